@@ -25,10 +25,12 @@ AR_F32, AR_BF16, AR_F16 = 0, 1, 2
 DTYPES = {"f32": AR_F32, "bf16": AR_BF16, "f16": AR_F16}
 AR_OK, AR_ERR_INVALID, AR_ERR_ALIGN, AR_ERR_TOO_LARGE, AR_ERR_CUDA, AR_ERR_FLAG_TIMEOUT, AR_ERR_WAIT_TIMEOUT = (
     0, -1, -2, -3, -4, -5, -6)
+AR_ERR_INDEX = -7
 (AR_OP_NONE, AR_OP_ONE_SHOT, AR_OP_TWO_SHOT, AR_OP_RING, AR_OP_LL_PACK, AR_OP_LL_UNPACK, AR_OP_LL_REDUCE,
  AR_OP_LL128_PACK, AR_OP_LL128_UNPACK, AR_OP_LL128_REDUCE, AR_OP_ALLREDUCE_RMSNORM, AR_OP_ONE_SHOT_PUSH,
  AR_OP_ONE_SHOT_COPYIN, AR_OP_RING_ROUNDED, AR_OP_TREE, AR_OP_RING_PERSISTENT, AR_OP_RING_CLUSTER,
- AR_OP_TREE_FUSED, AR_OP_RING_FUSED, AR_OP_RING_ROUNDED_FUSED) = range(20)
+ AR_OP_TREE_FUSED, AR_OP_RING_FUSED, AR_OP_RING_ROUNDED_FUSED, AR_OP_ALLREDUCE_BLOCK_NORM, AR_OP_ROPE_APPEND,
+ AR_OP_PAGED_ATTENTION) = range(23)
 AR_OPT_CTAS_PER_SM, AR_OPT_SPIN_NS, AR_OPT_ONE_SHOT_IMPL, AR_OPT_TIMING, AR_OPT_TIMING_PAUSE, AR_OPT_PDL = 1, 2, 3, 4, 5, 6
 AR_OPT_AUTO_POLICY, AR_OPT_AUTO_ALPHA_NS, AR_OPT_AUTO_BETA_MBS, AR_OPT_AUTO_HANDOFF = 7, 8, 9, 10
 AR_OPT_PUSH_STAGING, AR_OPT_REGISTERED, AR_OPT_PERSISTENT, AR_OPT_ABSENT_RANK = 11, 12, 13, 14
@@ -39,7 +41,8 @@ KERNELS = {1: "one_shot", 2: "reduce_scatter", 3: "all_gather", 4: "ring_rs_step
            11: "ll128_reduce", 12: "allreduce_rmsnorm", 13: "push", 14: "push_reduce",
            15: "ring_rs_step_rounded", 16: "tree_level", 17: "ring_persistent",
            18: "copyin", 19: "ring_cluster", 20: "tree_fused", 21: "ring_fused", 22: "ring_rounded_fused",
-           23: "two_shot"}
+           23: "two_shot", 24: "allreduce_block_norm", 25: "rope_append", 26: "attention_decode",
+           27: "attention_chunk"}
 
 # C symbols the header declares (checked by the CPU tests against include/ar.h)
 EXPORTS = (
@@ -49,7 +52,9 @@ EXPORTS = (
     "ar_check_args", "ar_strerror", "ar_timing", "ar_ll_pack_n", "ar_ll_unpack_n", "ar_ll128_pack_n",
     "ar_ll128_unpack_n", "ar_ring_noalloc", "ar_select", "ar_auto", "ar_allreduce_rmsnorm",
     "ar_one_shot_push", "ar_one_shot_copyin", "ar_ring_rounded", "ar_tree", "ar_ring_persistent",
-    "ar_ring_cluster", "ar_tree_fused", "ar_ring_fused", "ar_ring_rounded_fused",
+    "ar_ring_cluster", "ar_tree_fused", "ar_ring_fused", "ar_ring_rounded_fused", "ar_allreduce_block_norm",
+    "ar_kv_create", "ar_kv_destroy", "ar_rope_append", "ar_paged_attention", "ar_check_block_norm", "ar_check_kv",
+    "ar_check_rope_append", "ar_check_paged_attention",
 )
 
 
@@ -71,6 +76,24 @@ class StatusInfo(ctypes.Structure):
 class LaunchTime(ctypes.Structure):
     _fields_ = [("kernel", ctypes.c_int), ("op", ctypes.c_int), ("ms", ctypes.c_float),
                 ("hbm_bytes", ctypes.c_uint64), ("launches", ctypes.c_int)]
+
+
+class BlockNorm(ctypes.Structure):
+    _fields_ = [("residual", ctypes.c_void_p), ("post_weight", ctypes.c_void_p), ("gate", ctypes.c_void_p),
+                ("gate_stride", ctypes.c_size_t), ("pre_weight", ctypes.c_void_p), ("alpha", ctypes.c_float),
+                ("beta", ctypes.c_float), ("eps", ctypes.c_float)]
+
+
+class KvDesc(ctypes.Structure):
+    _fields_ = [("dtype", ctypes.c_int), ("kv_heads", ctypes.c_int), ("head_dim", ctypes.c_int),
+                ("page_size", ctypes.c_int), ("pages", ctypes.c_size_t), ("page_stride", ctypes.c_size_t),
+                ("head_stride", ctypes.c_size_t), ("token_stride", ctypes.c_size_t)]
+
+
+class Batch(ctypes.Structure):
+    _fields_ = [("tokens", ctypes.c_size_t), ("seqs", ctypes.c_int), ("max_new", ctypes.c_int),
+                ("q_start", ctypes.c_void_p), ("kv_len", ctypes.c_void_p), ("page_table", ctypes.c_void_p),
+                ("table_stride", ctypes.c_size_t)]
 
 
 class ArError(RuntimeError):
@@ -105,6 +128,19 @@ def lib() -> ctypes.CDLL:
                 "ar_select": ([i32, i32, sz, ctypes.c_double, ctypes.c_double, sz], i32),
                 "ar_auto": ([vp, pp, pp, sz, i32, vp], i32),
                 "ar_allreduce_rmsnorm": ([vp, pp, vp, vp, ctypes.c_float, pp, vp, sz, sz, i32, vp], i32),
+                "ar_allreduce_block_norm": ([vp, pp, ctypes.POINTER(BlockNorm), pp, vp, sz, sz, i32, vp], i32),
+                "ar_kv_create": ([vp, ctypes.POINTER(KvDesc), pp, pp, ctypes.POINTER(vp)], i32),
+                "ar_kv_destroy": ([vp], i32),
+                "ar_rope_append": ([vp, ctypes.POINTER(Batch), pp, pp, pp, pp, i32, sz, sz, sz, vp, sz, i32, i32,
+                                    vp], i32),
+                "ar_paged_attention": ([vp, ctypes.POINTER(Batch), pp, pp, i32, sz, sz, ctypes.c_float, i32, vp],
+                                       i32),
+                "ar_check_block_norm": ([i32, sz, pp, ctypes.POINTER(BlockNorm), pp, vp, sz, sz, i32], i32),
+                "ar_check_kv": ([i32, ctypes.POINTER(KvDesc), pp, pp], i32),
+                "ar_check_rope_append": ([i32, ctypes.POINTER(KvDesc), ctypes.POINTER(Batch), pp, pp, pp, pp, i32,
+                                          sz, sz, sz, vp, sz, i32, i32], i32),
+                "ar_check_paged_attention": ([i32, ctypes.POINTER(KvDesc), ctypes.POINTER(Batch), pp, pp, i32, sz,
+                                              sz, ctypes.c_float, i32], i32),
                 "ar_one_shot_push": ([vp, pp, pp, sz, i32, vp], i32),
                 "ar_one_shot_copyin": ([vp, pp, pp, sz, i32, vp], i32),
                 "ar_ring_rounded": ([vp, pp, pp, sz, i32, vp], i32),
@@ -255,6 +291,50 @@ def ar_allreduce_rmsnorm(h, ins, residual, weight, eps: float, norm_outs, residu
                                       _addr(residual_out), tokens, hidden, _dtype(dtype), _stream(stream))
 
 
+def ar_allreduce_block_norm(h, ins, residual, post_weight, gate, gate_stride: int, pre_weight, alpha: float,
+                            beta: float, eps: float, norm_outs, residual_out, tokens: int, hidden: int, dtype,
+                            stream=None) -> int:
+    p = BlockNorm(_addr(residual), _addr(post_weight), _addr(gate), gate_stride, _addr(pre_weight), alpha, beta, eps)
+    return lib().ar_allreduce_block_norm(h, _ptr_array(ins), ctypes.byref(p), _ptr_array(norm_outs),
+                                         _addr(residual_out), tokens, hidden, _dtype(dtype), _stream(stream))
+
+
+def ar_kv_create(h, ks, vs, dtype, kv_heads: int, head_dim: int, page_size: int, pages: int, page_stride: int,
+                 head_stride: int, token_stride: int) -> int:
+    """Returns the registration of the ranks' caches (an opaque address); raises ArError on failure.
+    Strides are in elements.  The caches must outlive it."""
+    d = KvDesc(_dtype(dtype), kv_heads, head_dim, page_size, pages, page_stride, head_stride, token_stride)
+    kv = ctypes.c_void_p()
+    rc = lib().ar_kv_create(h, ctypes.byref(d), _ptr_array(ks), _ptr_array(vs), ctypes.byref(kv))
+    if rc != AR_OK:
+        raise ArError(rc, "ar_kv_create")
+    return kv.value
+
+
+def ar_kv_destroy(kv: int) -> int:
+    return lib().ar_kv_destroy(kv)
+
+
+def ar_batch(tokens: int, seqs: int, max_new: int, q_start, kv_len, page_table, table_stride: int) -> Batch:
+    """ar_batch_t over int32 device arrays (which must outlive the calls that use it)."""
+    return Batch(tokens, seqs, max_new, _addr(q_start), _addr(kv_len), _addr(page_table), table_stride)
+
+
+def ar_rope_append(kv, batch: Batch, qs, ks, vs, q_outs, q_heads: int, q_stride: int, kv_stride: int,
+                   q_out_stride: int, cos_sin, max_positions: int, rot_dim: int, interleaved: int = 0,
+                   stream=None) -> int:
+    return lib().ar_rope_append(kv, ctypes.byref(batch), None if qs is None else _ptr_array(qs), _ptr_array(ks),
+                                _ptr_array(vs), None if q_outs is None else _ptr_array(q_outs), q_heads, q_stride,
+                                kv_stride, q_out_stride, _addr(cos_sin), max_positions, rot_dim, interleaved,
+                                _stream(stream))
+
+
+def ar_paged_attention(kv, batch: Batch, qs, outs, q_heads: int, q_stride: int, out_stride: int, scale: float,
+                       window: int = 0, stream=None) -> int:
+    return lib().ar_paged_attention(kv, ctypes.byref(batch), _ptr_array(qs), _ptr_array(outs), q_heads, q_stride,
+                                    out_stride, scale, window, _stream(stream))
+
+
 def ar_ring_noalloc(n_ranks: int, ins, outs, count: int, dtype, stream=None) -> int:
     """ar_ring without a handle or any allocation (static 32 MiB scratch in the library)."""
     return lib().ar_ring_noalloc(n_ranks, _ptr_array(ins), _ptr_array(outs), count, _dtype(dtype), _stream(stream))
@@ -338,6 +418,33 @@ def ar_check_args(op: int, n_ranks: int, max_bytes: int, ins, outs, count: int, 
     pin = _ptr_array(ins) if ins is not None else None
     pout = _ptr_array(outs) if outs is not None else None
     return lib().ar_check_args(op, n_ranks, max_bytes, pin, pout, count, _dtype(dtype))
+
+
+def ar_check_block_norm(n_ranks: int, max_bytes: int, ins, residual, post_weight, gate, gate_stride: int, pre_weight,
+                        alpha: float, beta: float, eps: float, norm_outs, residual_out, tokens: int, hidden: int,
+                        dtype) -> int:
+    p = BlockNorm(_addr(residual), _addr(post_weight), _addr(gate), gate_stride, _addr(pre_weight), alpha, beta, eps)
+    return lib().ar_check_block_norm(n_ranks, max_bytes, _ptr_array(ins), ctypes.byref(p), _ptr_array(norm_outs),
+                                     _addr(residual_out), tokens, hidden, _dtype(dtype))
+
+
+def ar_check_kv(n_ranks: int, desc: KvDesc, ks, vs) -> int:
+    return lib().ar_check_kv(n_ranks, ctypes.byref(desc), _ptr_array(ks), _ptr_array(vs))
+
+
+def ar_check_rope_append(n_ranks: int, desc: KvDesc, batch: Batch, qs, ks, vs, q_outs, q_heads: int, q_stride: int,
+                         kv_stride: int, q_out_stride: int, cos_sin, max_positions: int, rot_dim: int,
+                         interleaved: int = 0) -> int:
+    return lib().ar_check_rope_append(n_ranks, ctypes.byref(desc), ctypes.byref(batch),
+                                      None if qs is None else _ptr_array(qs), _ptr_array(ks), _ptr_array(vs),
+                                      None if q_outs is None else _ptr_array(q_outs), q_heads, q_stride, kv_stride,
+                                      q_out_stride, _addr(cos_sin), max_positions, rot_dim, interleaved)
+
+
+def ar_check_paged_attention(n_ranks: int, desc: KvDesc, batch: Batch, qs, outs, q_heads: int, q_stride: int,
+                             out_stride: int, scale: float, window: int = 0) -> int:
+    return lib().ar_check_paged_attention(n_ranks, ctypes.byref(desc), ctypes.byref(batch), _ptr_array(qs),
+                                          _ptr_array(outs), q_heads, q_stride, out_stride, scale, window)
 
 
 def ar_timing(h, max_records: int = 1 << 20) -> list[tuple[str, int, float, int, int]]:

@@ -8,6 +8,7 @@
 #include <new>
 
 #include "common.cuh"
+#include "layer.h"
 
 using namespace argb;
 
@@ -77,6 +78,39 @@ int check_multi(int op, int n, size_t max_bytes, const void* const* in, void* co
             if (q == r) continue;
             if (overlap(out[r], out[q], bytes) || overlap(out[r], in[q], bytes)) return AR_ERR_INVALID;
         }
+    }
+    return AR_OK;
+}
+
+int check_block_norm(int n, size_t max_bytes, const void* const* in, const ar_block_norm_t* p, void* const* norm_out,
+                     const void* residual_out, size_t tokens, size_t hidden, int dt)
+{
+    if (!p) return AR_ERR_INVALID;
+    if (dt != AR_F32 && dt != AR_BF16 && dt != AR_F16) return AR_ERR_INVALID;
+    if (!(p->eps >= 0.0f) || p->eps == INFINITY || !std::isfinite(p->alpha) || !std::isfinite(p->beta))
+        return AR_ERR_INVALID;
+    const size_t e = elem_bytes(dt);
+    if (!block_norm_fits(hidden, dt)) return AR_ERR_INVALID;
+    if (tokens > (size_t)INT_MAX / 16u || tokens > SIZE_MAX / hidden / 128u) return AR_ERR_TOO_LARGE;
+    const size_t count = tokens * hidden;
+    if (int rc = check_multi(AR_OP_ONE_SHOT, n, max_bytes, in, norm_out, count, dt)) return rc;
+    if (!p->residual || !p->pre_weight || !residual_out) return AR_ERR_INVALID;
+    if (p->gate && (p->gate_stride % (16u / e) != 0 || (p->gate_stride != 0 && p->gate_stride < hidden) ||
+                    p->gate_stride > ((size_t)1 << 40) / (tokens ? tokens : 1)))
+        return AR_ERR_INVALID;
+    if (!aligned16(p->residual) || !aligned16(p->pre_weight) || !aligned16(residual_out) ||
+        !aligned16(p->post_weight) || !aligned16(p->gate))
+        return AR_ERR_ALIGN;
+    const size_t S = count * e, W = hidden * e;
+    const size_t G = tokens ? ((tokens - 1) * p->gate_stride + hidden) * e : 0;
+    if (residual_out != p->residual && overlap(residual_out, p->residual, S)) return AR_ERR_INVALID;
+    for (int r = -1; r < n; ++r) {   // every output, residual_out first
+        const void* o = r < 0 ? residual_out : norm_out[r];
+        if (overlap_sized(o, S, p->pre_weight, W) || (p->post_weight && overlap_sized(o, S, p->post_weight, W)) ||
+            (p->gate && overlap_sized(o, S, p->gate, G)))
+            return AR_ERR_INVALID;
+        if (r >= 0 && (overlap(residual_out, in[r], S) || overlap(residual_out, o, S) || overlap(o, p->residual, S)))
+            return AR_ERR_INVALID;
     }
     return AR_OK;
 }
@@ -315,6 +349,8 @@ static Handle* get(ar_handle hd)
     return (hd && hd->magic == kMagic) ? &hd->h : nullptr;
 }
 
+Handle* argb::handle_of(ar_handle hd) { return get(hd); }
+
 typedef int (*multi_launcher)(Handle&, const void* const*, void* const*, size_t, int, cudaStream_t, int*);
 
 static int all_reduce_call(int op, multi_launcher fn, ar_handle hd, const void* const* in, void* const* out,
@@ -397,6 +433,7 @@ const char* ar_strerror(int code)
     case AR_ERR_CUDA: return "CUDA runtime error";
     case AR_ERR_FLAG_TIMEOUT: return "LL/LL128 flag not seen within the spin limit";
     case AR_ERR_WAIT_TIMEOUT: return "a kernel's bounded wait (its bulk copies, or a peer freeing a slot) ran out";
+    case AR_ERR_INDEX: return "a page, length or position in device memory is out of range";
     default: return "unknown error code";
     }
 }
@@ -784,6 +821,34 @@ int ar_allreduce_rmsnorm(ar_handle hd, const void* const* in, const void* residu
     if (count) h->last.hbm_read_bytes += W;
     h->last_stream = (cudaStream_t)stream;
     return AR_OK;
+}
+
+int ar_allreduce_block_norm(ar_handle hd, const void* const* in, const ar_block_norm_t* p, void* const* norm_out,
+                            void* residual_out, size_t tokens, size_t hidden, ar_dtype dt, ar_stream_t stream)
+{
+    Handle* h = get(hd);
+    if (!h) return AR_ERR_INVALID;
+    if (int rc = check_block_norm(h->n, h->max_bytes, in, p, norm_out, residual_out, tokens, hidden, dt)) return rc;
+    const size_t count = tokens * hidden, S = count * elem_bytes(dt), W = hidden * elem_bytes(dt);
+    int rc = AR_OK;
+    h->timing.op = AR_OP_ALLREDUCE_BLOCK_NORM;
+    if (count)
+        rc = on_device(*h, [&] {
+            return launch_block_norm(*h, in, *p, norm_out, residual_out, tokens, hidden, dt, (cudaStream_t)stream);
+        });
+    if (rc != AR_OK) return rc;
+    plan(AR_OP_ALLREDUCE_RMSNORM, h->n, count, dt, &h->last);   // the same rank, residual and output bytes
+    h->last.op = AR_OP_ALLREDUCE_BLOCK_NORM;
+    if (count)
+        h->last.hbm_read_bytes += W * (p->post_weight ? 2 : 1) + (p->gate ? (p->gate_stride ? S : W) : 0);
+    h->last_stream = (cudaStream_t)stream;
+    return AR_OK;
+}
+
+int ar_check_block_norm(int n_ranks, size_t max_bytes, const void* const* in, const ar_block_norm_t* p,
+                        void* const* norm_out, void* residual_out, size_t tokens, size_t hidden, ar_dtype dt)
+{
+    return check_block_norm(n_ranks, max_bytes, in, p, norm_out, residual_out, tokens, hidden, dt);
 }
 
 int ar_select(int policy, int n_ranks, size_t bytes_per_rank, double alpha_s, double beta, size_t handoff_bytes)

@@ -1,0 +1,505 @@
+// Paged attention for few query rows per kv head: decode steps of one token
+// a sequence, or of a few drafted ones.
+//
+// A row tile holds at most 16 rows (new tokens x the query heads that share a
+// kv head), and every key and value of the sequence is read for it once, so
+// the bound is HBM: 4 D bytes per key and head against 64 D flops on the tile,
+// 16 flops per byte where the machine's tensor cores could do 280.  The
+// products therefore use mma.sync m16n8k16, whose 16 rows waste least, and the
+// design is about keeping enough copies in flight: one warp issues tensor
+// copies of 64-key tiles (K and V) into a ring of stages, two CTAs of an SM
+// together holding about 190 KB of them, and four warps each take 16 keys of
+// every tile with their own running maximum, sum and output accumulators, so
+// nothing but the ring's barriers is shared until a row tile's keys end.
+//
+// Softmax in one pass, base 2: with x = scale log2(e) (q . k), a running
+// reference m, p = 2^(x - m), l = sum p, o = sum p v.  m moves only when a row's
+// maximum passes it by more than 8: p stays below 2^8, which fp32 sums, fp16
+// and bf16 all hold without loss, and the accumulators are seldom rescaled.
+//
+// Split of the keys: split_work cuts all key tiles of the call into equal runs,
+// one per CTA.  Row tiles that lie in several runs leave their parts (o, m, l,
+// fp32) in the workspace, and the CTA that arrives last joins them in the order
+// of the keys, so the result does not depend on which one that is.
+#include "paged.cuh"
+
+namespace argb {
+namespace {
+
+constexpr int kKeys = 64;                    // keys of a tile
+constexpr int kWarps = 4;                    // consumers, 16 keys each
+constexpr int kTh = 32 * (kWarps + 1);
+constexpr int kRows = 16;
+constexpr int kCtas = 2;                     // per SM
+constexpr float kSlack = 8.0f;               // log2 of how far p may pass 1
+
+template <int D> constexpr int kTileBytes = kKeys * D * 2;
+template <int D> constexpr int kStages = D == 128 ? 3 : 6;
+template <int D> constexpr int kPartFloats = kRows * (D + 2);
+
+struct DecodeShared {
+    uint64_t full[6], empty[6];
+    float m[kWarps][kRows], l[kWarps][kRows];
+    SplitShared split;
+    int gave_up, last;
+};
+static_assert(sizeof(DecodeShared) <= 1024, "the shared memory of two CTAs fits one SM exactly");
+
+// stages, then two accumulator buffers, then DecodeShared
+template <int D> constexpr int kSmem = kStages<D> * 2 * kTileBytes<D> + 2 * kRows * D * 4 + 1024;
+
+struct DecodeArgs {
+    const void* q[kMaxRanks];
+    void* out[kMaxRanks];
+    const CUtensorMap* maps;
+    float* partial;
+    unsigned* arrived;
+    size_t q_stride, out_stride;
+    float scale_log2;
+    int n, kv_heads, group;                  // query heads per kv head
+    int tile_heads, head_groups, tm;         // query heads and new tokens of a row tile
+    int box_tokens, min_units;
+};
+
+template <int DT>
+__device__ __forceinline__ void mma16816(float* d, const uint32_t* a, uint32_t b0, uint32_t b1)
+{
+    if constexpr (DT == AR_BF16)
+        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+                     "{%0,%1,%2,%3};"
+                     : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+                     : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+    else
+        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+                     "{%0,%1,%2,%3};"
+                     : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+                     : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ void ldmatrix4(uint32_t* r, uint32_t addr)
+{
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+
+__device__ __forceinline__ void ldmatrix4_trans(uint32_t* r, uint32_t addr)
+{
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+
+__device__ __forceinline__ void consumers_sync() { asm volatile("bar.sync 1, %0;" ::"n"(32 * kWarps) : "memory"); }
+
+// A segment's rows: rank, kv head, first query head and number of heads, first
+// new token, number of rows (row i: token i / heads, head i % heads).
+struct RowTile {
+    int rank, kv_head, head0, heads, tok0, rows;
+};
+
+__device__ __forceinline__ RowTile row_tile(const DecodeArgs& a, const Segment& seg)
+{
+    RowTile r;
+    const int hg = seg.head % a.head_groups, kvh = seg.head / a.head_groups;
+    r.kv_head = kvh % a.kv_heads;
+    r.rank = kvh / a.kv_heads;
+    r.heads = min(a.tile_heads, a.group - hg * a.tile_heads);
+    r.head0 = r.kv_head * a.group + hg * a.tile_heads;
+    r.tok0 = seg.t * a.tm;
+    r.rows = min(a.tm, seg.q.nq - r.tok0) * r.heads;
+    return r;
+}
+
+template <int D>
+__device__ void produce(const DecodeArgs& a, const BatchArgs& b, const Cursor& cur, uint8_t* stages, DecodeShared* sh,
+                        DevStatus* st)
+{
+    const int lane = threadIdx.x & 31;
+    const int per_page = kKeys / a.box_tokens;         // boxes of a tile along the keys: 1, 2 or 4
+    const int panels = D / 64;
+    // lane -> one copy of the tile
+    const int box = lane % per_page, panel = (lane / per_page) % panels, is_v = lane / (per_page * panels);
+    const bool mine = is_v < 2;
+    Walk<kKeys> walk(cur);
+    Segment seg;
+    int stage = 0;
+    uint32_t phase = 0;
+    uint32_t issued = 0;
+    bool ok = true;
+    while (ok && walk.next(b, a.tm, seg, st)) {
+        const RowTile rt = row_tile(a, seg);
+        const CUtensorMap* map = a.maps + (is_v ? a.n : 0) + rt.rank;
+        const int32_t* row = b.table + (size_t)seg.s * b.table_stride;
+        for (int j = seg.j0; ok && j < seg.j1; ++j) {
+            const int key = j * kKeys + box * a.box_tokens;
+            bool copy = mine && key < seg.span.key_hi && key + a.box_tokens > seg.span.key_lo;
+            int page = 0;
+            if (copy) {
+                page = row[key >> b.page_shift];
+                if (page < 0 || page >= b.pages) {
+                    report_index(st);
+                    copy = false;
+                }
+            }
+            if (issued >= (uint32_t)kStages<D>) ok = wait_or_give_up(&sh->empty[stage], phase ^ 1, &sh->gave_up, st);
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) break;
+            const int copies = __popc(__ballot_sync(0xffffffffu, copy));
+            if (lane == 0) mbar_arrive_expect_tx(&sh->full[stage], (uint32_t)copies * a.box_tokens * 128u);
+            __syncwarp();
+            if (copy)
+                page_copy(stages + (size_t)stage * 2 * kTileBytes<D> + is_v * kTileBytes<D> + panel * (kKeys * 128) +
+                              box * a.box_tokens * 128,
+                          map, panel * 64, key & ((1 << b.page_shift) - 1), rt.kv_head, page, &sh->full[stage]);
+            ++issued;
+            if (++stage == kStages<D>) {
+                stage = 0;
+                phase ^= 1;
+            }
+        }
+    }
+    // after a wait that ran out the copies in flight still land in this CTA's shared memory
+    if (!ok)
+        for (uint32_t k = 0; k < issued && k < (uint32_t)kStages<D>; ++k) {
+            stage = stage == 0 ? kStages<D> - 1 : stage - 1;
+            if (stage == kStages<D> - 1) phase ^= 1;
+            wait_a_second(&sh->full[stage], phase, nullptr);
+        }
+}
+
+template <int DT, int D>
+__device__ void consume(const DecodeArgs& a, const BatchArgs& b, const Cursor& cur, uint8_t* stages, float* acc,
+                        DecodeShared* sh, DevStatus* st)
+{
+    using T = typename Payload<DT>::scalar_t;
+    constexpr int KS = D / 16;      // k-steps of q . k
+    constexpr int NT = D / 8;       // 8-wide column tiles of the output
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int r0 = lane >> 2, col = (lane & 3) * 2;
+    Walk<kKeys> walk(cur);
+    Segment seg;
+    int stage = 0;
+    uint32_t phase = 0;
+    bool ok = true;   // false once a wait ran out: the warps still meet at every barrier, without the work
+    while (walk.next(b, a.tm, seg, st)) {
+        const RowTile rt = row_tile(a, seg);
+        const T* qp = static_cast<const T*>(a.q[rt.rank]) + (size_t)rt.head0 * D;
+        // rows of this thread: r0 and r0 + 8
+        int limit[2], lower[2];
+        uint32_t qf[KS][4];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int r = r0 + 8 * i;
+            const bool there = r < rt.rows;
+            const int tok = rt.tok0 + r / rt.heads, hd = r % rt.heads;
+            limit[i] = there ? seg.q.c0 + tok + 1 : 0;
+            lower[i] = b.window > 0 ? limit[i] - b.window : 0;
+            const T* row = qp + (size_t)(seg.q.q0 + tok) * a.q_stride + (size_t)hd * D + col;
+#pragma unroll
+            for (int k = 0; k < KS; ++k) {
+                qf[k][i] = there ? *reinterpret_cast<const uint32_t*>(row + 16 * k) : 0u;
+                qf[k][2 + i] = there ? *reinterpret_cast<const uint32_t*>(row + 16 * k + 8) : 0u;
+            }
+        }
+        // keys that every row of the tile sees
+        const int last_tok = rt.tok0 + (rt.rows - 1) / rt.heads;
+        const int all_hi = seg.q.c0 + rt.tok0 + 1;
+        const int all_lo = b.window > 0 ? seg.q.c0 + last_tok + 1 - b.window : 0;
+        float o[NT][4], m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};
+#pragma unroll
+        for (int n = 0; n < NT; ++n) o[n][0] = o[n][1] = o[n][2] = o[n][3] = 0.0f;
+
+        for (int j = seg.j0; j < seg.j1; ++j) {
+            const int key0 = j * kKeys + warp * 16;
+            if (ok) ok = wait_or_give_up(&sh->full[stage], phase, &sh->gave_up, st);
+            ok = __all_sync(0xffffffffu, ok);
+            if (ok && key0 < seg.span.key_hi && key0 + 16 > seg.span.key_lo) {
+                const uint32_t kbase = smem_addr(stages + (size_t)stage * 2 * kTileBytes<D>);
+                const uint32_t vbase = kbase + kTileBytes<D>;
+                if (key0 + 16 > seg.span.key_hi || key0 < seg.span.key_lo) {
+                    // slots of these pages that no row sees may hold anything: their values count as 0
+                    for (int i = lane; i < 16 * (D / 8); i += 32) {
+                        const int r = i / (D / 8), c = i % (D / 8);
+                        if (key0 + r >= seg.span.key_hi || key0 + r < seg.span.key_lo) {
+                            const uint32_t at = swizzled(vbase + (c >> 3) * (kKeys * 128), warp * 16 + r, c & 7);
+                            asm volatile("st.shared.v4.b32 [%0], {%1,%1,%1,%1};" ::"r"(at), "r"(0) : "memory");
+                        }
+                    }
+                    __syncwarp();
+                    fence_proxy_async();   // before the next copy into this stage
+                }
+                float s[2][4] = {};
+                const int kr = warp * 16 + (lane & 7) + ((lane >> 4) << 3);   // key rows 0-7, then 8-15
+                const int kc = (lane >> 3) & 1;                               // low, high 8 of the k-step
+#pragma unroll
+                for (int k = 0; k < KS; ++k) {
+                    uint32_t kf[4];
+                    const int c = 2 * k + kc;
+                    ldmatrix4(kf, swizzled(kbase + (c >> 3) * (kKeys * 128), kr, c & 7));
+                    mma16816<DT>(s[0], qf[k], kf[0], kf[1]);
+                    mma16816<DT>(s[1], qf[k], kf[2], kf[3]);
+                }
+                const bool masked = key0 + 16 > all_hi || key0 < all_lo;
+                float mx[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+                for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        float x = s[nt][e] * a.scale_log2;
+                        if (masked) {
+                            const int key = key0 + 8 * nt + col + (e & 1);
+                            if (key >= limit[e >> 1] || key < lower[e >> 1]) x = -INFINITY;
+                        }
+                        s[nt][e] = x;
+                        mx[e >> 1] = fmaxf(mx[e >> 1], x);
+                    }
+                bool move = false;
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    mx[i] = fmaxf(mx[i], __shfl_xor_sync(0xffffffffu, mx[i], 1));
+                    mx[i] = fmaxf(mx[i], __shfl_xor_sync(0xffffffffu, mx[i], 2));
+                    move |= mx[i] > m[i] + kSlack;
+                }
+                if (__any_sync(0xffffffffu, move)) {
+                    float f[2];
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const float to = fmaxf(m[i], mx[i]);
+                        f[i] = m[i] == -INFINITY ? 0.0f : ex2(m[i] - to);
+                        m[i] = to;
+                        l[i] *= f[i];
+                    }
+#pragma unroll
+                    for (int n = 0; n < NT; ++n) {
+                        o[n][0] *= f[0];
+                        o[n][1] *= f[0];
+                        o[n][2] *= f[1];
+                        o[n][3] *= f[1];
+                    }
+                }
+                uint32_t pf[4];
+                float p[2][4];
+#pragma unroll
+                for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const float ref = m[e >> 1] == -INFINITY ? 0.0f : m[e >> 1];
+                        p[nt][e] = ex2(s[nt][e] - ref);
+                        l[e >> 1] += p[nt][e];
+                    }
+                // rounded to the cache's type: the product's operand (at most half a step of it each)
+                pf[0] = Payload<DT>::narrow(&p[0][0]);
+                pf[1] = Payload<DT>::narrow(&p[0][2]);
+                pf[2] = Payload<DT>::narrow(&p[1][0]);
+                pf[3] = Payload<DT>::narrow(&p[1][2]);
+                const int vr = warp * 16 + (lane & 15);     // keys 0-7, 8-15
+                const int vc = lane >> 4;                   // columns 0-7, 8-15
+#pragma unroll
+                for (int n = 0; n < NT; n += 2) {
+                    uint32_t vf[4];
+                    const int c = n + vc;
+                    ldmatrix4_trans(vf, swizzled(vbase + (c >> 3) * (kKeys * 128), vr, c & 7));
+                    mma16816<DT>(o[n], pf, vf[0], vf[1]);
+                    mma16816<DT>(o[n + 1], pf, vf[2], vf[3]);
+                }
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sh->empty[stage]);
+            if (++stage == kStages<D>) {
+                stage = 0;
+                phase ^= 1;
+            }
+        }
+
+        // join the four warps: maxima and sums, then the accumulators, warps 0 and 2 first
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            l[i] += __shfl_xor_sync(0xffffffffu, l[i], 1);
+            l[i] += __shfl_xor_sync(0xffffffffu, l[i], 2);
+            if ((lane & 3) == 0) {
+                sh->m[warp][r0 + 8 * i] = m[i];
+                sh->l[warp][r0 + 8 * i] = l[i];
+            }
+        }
+        consumers_sync();
+        float f[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            float top = -INFINITY;
+            for (int w = 0; w < kWarps; ++w) top = fmaxf(top, sh->m[w][r0 + 8 * i]);
+            f[i] = m[i] == -INFINITY ? 0.0f : ex2(m[i] - top);
+        }
+        float* mine = acc + (warp >> 1) * (kRows * D);
+#pragma unroll
+        for (int turn = 0; turn < 2; ++turn) {
+            if ((warp & 1) == turn) {
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        float2* at = reinterpret_cast<float2*>(mine + (r0 + 8 * i) * D + 8 * n + col);
+                        float2 x = make_float2(o[n][2 * i] * f[i], o[n][2 * i + 1] * f[i]);
+                        if (turn == 1) {
+                            const float2 y = *at;
+                            x.x += y.x;
+                            x.y += y.y;
+                        }
+                        *at = x;
+                    }
+            }
+            consumers_sync();
+        }
+        T* op = static_cast<T*>(a.out[rt.rank]) + (size_t)rt.head0 * D;
+        auto store_row4 = [&](int r, int d, const float4& x) {
+            const int tok = rt.tok0 + r / rt.heads, hd = r % rt.heads;
+            const float v[4] = {x.x, x.y, x.z, x.w};
+            uint2 w = make_uint2(Payload<DT>::narrow(v), Payload<DT>::narrow(v + 2));
+            *reinterpret_cast<uint2*>(op + (size_t)(seg.q.q0 + tok) * a.out_stride + (size_t)hd * D + d) = w;
+        };
+        float* part = a.partial + (size_t)seg.slot * kPartFloats<D>;
+        for (int i = tid; i < rt.rows * (D / 4); i += 32 * kWarps) {
+            const int r = i / (D / 4), d = i % (D / 4) * 4;
+            const float4 x = *reinterpret_cast<const float4*>(acc + r * D + d);
+            const float4 y = *reinterpret_cast<const float4*>(acc + kRows * D + r * D + d);
+            float4 z = make_float4(x.x + y.x, x.y + y.y, x.z + y.z, x.w + y.w);
+            float top = -INFINITY, sum = 0.0f;
+            for (int w = 0; w < kWarps; ++w) top = fmaxf(top, sh->m[w][r]);
+            for (int w = 0; w < kWarps; ++w)
+                sum += sh->m[w][r] == -INFINITY ? 0.0f : sh->l[w][r] * ex2(sh->m[w][r] - top);
+            if (seg.whole) {
+                const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+                store_row4(r, d, make_float4(z.x * inv, z.y * inv, z.z * inv, z.w * inv));
+            } else {
+                __stcg(reinterpret_cast<float4*>(part + r * D + d), z);
+                if (d == 0) {
+                    __stcg(part + kRows * D + r, top);
+                    __stcg(part + kRows * D + kRows + r, sum);
+                }
+            }
+        }
+        if (!seg.whole) {
+            __threadfence();
+            consumers_sync();
+            if (tid == 0) {
+                const unsigned before = atomicAdd(&a.arrived[seg.first_cta], 1u);
+                sh->last = before + 1 == seg.parts;
+                if (sh->last) a.arrived[seg.first_cta] = 0;   // for the next call
+            }
+            consumers_sync();
+            if (sh->last) {
+                __threadfence();
+                for (int i = tid; i < rt.rows * (D / 4); i += 32 * kWarps) {
+                    const int r = i / (D / 4), d = i % (D / 4) * 4;
+                    float top = -INFINITY;
+                    for (unsigned k = 0; k < seg.parts; ++k)
+                        top = fmaxf(top, __ldcg(a.partial + (size_t)part_slot(seg.first_cta, k) * kPartFloats<D> +
+                                                kRows * D + r));
+                    float4 z = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                    float sum = 0.0f;
+                    for (unsigned k = 0; k < seg.parts; ++k) {
+                        const float* from = a.partial + (size_t)part_slot(seg.first_cta, k) * kPartFloats<D>;
+                        const float pm = __ldcg(from + kRows * D + r);
+                        const float w = pm == -INFINITY ? 0.0f : ex2(pm - top);
+                        const float4 x = __ldcg(reinterpret_cast<const float4*>(from + r * D + d));
+                        z.x = fmaf(x.x, w, z.x);
+                        z.y = fmaf(x.y, w, z.y);
+                        z.z = fmaf(x.z, w, z.z);
+                        z.w = fmaf(x.w, w, z.w);
+                        sum = fmaf(__ldcg(from + kRows * D + kRows + r), w, sum);
+                    }
+                    const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+                    store_row4(r, d, make_float4(z.x * inv, z.y * inv, z.z * inv, z.w * inv));
+                }
+            }
+        }
+        consumers_sync();   // the buffers are free for the next row tile
+    }
+}
+
+template <int DT, int D>
+__global__ void __launch_bounds__(kTh, kCtas)
+attention_decode_kernel(const __grid_constant__ DecodeArgs a, const BatchArgs b, DevStatus* st)
+{
+    extern __shared__ __align__(1024) uint8_t smem[];
+    float* acc = reinterpret_cast<float*>(smem + kStages<D> * 2 * kTileBytes<D>);
+    DecodeShared* sh = reinterpret_cast<DecodeShared*>(acc + 2 * kRows * D);
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < kStages<D>; ++i) {
+            mbar_init(&sh->full[i], 1);
+            mbar_init(&sh->empty[i], kWarps);
+        }
+        mbar_init_fence();
+        sh->gave_up = 0;
+    }
+    pdl_acquire();
+    const Cursor cur =
+        split_work<kKeys, kTh>(b, a.tm, a.n * a.kv_heads * a.head_groups, a.min_units, &sh->split, st);
+    if (cur.g >= cur.end) {
+        pdl_release();
+        return;
+    }
+    if (threadIdx.x >= 32 * kWarps)
+        produce<D>(a, b, cur, smem, sh, st);
+    else
+        consume<DT, D>(a, b, cur, smem, acc, sh, st);
+    pdl_release();
+}
+
+}  // namespace
+
+size_t attention_decode_partial_floats(const Handle& h, int head_dim)
+{
+    return (size_t)(2 * kCtas * h.sm_count) * (size_t)(kRows * (head_dim + 2));
+}
+
+size_t attention_decode_counters(const Handle& h) { return (size_t)(kCtas * h.sm_count); }
+
+int launch_attention_decode(KvCache& kv, const ar_batch_t& b, const AttnCall& c, int window, cudaStream_t s)
+{
+    Handle& h = *kv.h;
+    DecodeArgs a{};
+    for (int r = 0; r < h.n; ++r) {
+        a.q[r] = c.q[r];
+        a.out[r] = c.out[r];
+    }
+    a.maps = kv.maps;
+    a.partial = kv.partial;
+    a.arrived = kv.arrived;
+    a.q_stride = c.q_stride;
+    a.out_stride = c.out_stride;
+    a.scale_log2 = c.scale * 1.4426950408889634f;
+    a.n = h.n;
+    a.kv_heads = kv.d.kv_heads;
+    a.group = c.q_heads / kv.d.kv_heads;
+    a.tile_heads = a.group < kRows ? a.group : kRows;
+    a.head_groups = (a.group + a.tile_heads - 1) / a.tile_heads;
+    a.tm = kRows / a.tile_heads;
+    a.box_tokens = kv.box_tokens;
+    a.min_units = 2;
+    const uint64_t moved = (uint64_t)h.n * b.tokens * c.q_heads * kv.d.head_dim * 2u * 2u;
+    auto run = [&](auto dtc, auto dc) -> int {
+        constexpr int DT = decltype(dtc)::value, D = decltype(dc)::value;
+        static std::atomic<uint32_t> attr_done{0};
+        if (!once_per_device(attr_done, [&] {
+                return cudaFuncSetAttribute(attention_decode_kernel<DT, D>,
+                                            cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem<D>) == cudaSuccess;
+            }))
+            return AR_ERR_CUDA;
+        rec_begin(h, s);
+        const cudaError_t e = launch_kernel(h, attention_decode_kernel<DT, D>, dim3((unsigned)(kCtas * h.sm_count)),
+                                            dim3(kTh), kSmem<D>, s, a, batch_args(kv, b, window), h.status);
+        rec_end(h, s, AR_K_ATTENTION_DECODE, moved);
+        return e == cudaSuccess ? launch_status() : AR_ERR_CUDA;
+    };
+    using BF = std::integral_constant<int, AR_BF16>;
+    using HF = std::integral_constant<int, AR_F16>;
+    using D64 = std::integral_constant<int, 64>;
+    using D128 = std::integral_constant<int, 128>;
+    if (kv.d.dtype == AR_BF16) return kv.d.head_dim == 128 ? run(BF{}, D128{}) : run(BF{}, D64{});
+    return kv.d.head_dim == 128 ? run(HF{}, D128{}) : run(HF{}, D64{});
+}
+
+}  // namespace argb

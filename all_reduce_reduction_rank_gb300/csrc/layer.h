@@ -1,0 +1,79 @@
+// Host-side internals of the calls around the all-reduce in a tensor-parallel
+// layer (block norm, rotation and append, paged attention).  Not part of the
+// C-ABI (that is include/ar.h).
+#pragma once
+
+#include <cuda.h>
+
+#include "internal.h"
+
+namespace argb {
+
+constexpr int kAttnTileRows = 128;   // query rows of one tensor-core tile of the chunk kernel
+constexpr int kMaxGroup = 64;        // query heads per kv head
+
+// The registered caches of a handle's ranks (ar_kv).
+struct KvCache {
+    Handle* h = nullptr;
+    ar_kv_desc_t d{};
+    int box_tokens = 0;              // tokens of one tensor copy: min(page_size, 64)
+    void* k[kMaxRanks] = {};
+    void* v[kMaxRanks] = {};
+    CUtensorMap* maps = nullptr;     // device: n maps of K, then n of V
+    float* partial = nullptr;        // device: partial results of rows split over CTAs
+    unsigned* arrived = nullptr;     // device: partials arrived, by the CTA in which the rows' first key tile lies
+};
+
+// A call's batch and cache geometry, passed by value to the kernels.
+struct BatchArgs {
+    const int32_t* q_start;
+    const int32_t* kv_len;
+    const int32_t* table;
+    size_t table_stride;
+    int tokens, seqs;
+    int page_shift;                  // log2(page_size)
+    int pages;
+    int window;                      // 0: none
+};
+
+inline BatchArgs batch_args(const KvCache& kv, const ar_batch_t& b, int window)
+{
+    int shift = 4;
+    while ((1 << shift) < kv.d.page_size) ++shift;
+    return BatchArgs{b.q_start, b.kv_len, b.page_table, b.table_stride, (int)b.tokens, b.seqs, shift,
+                     (int)kv.d.pages, window};
+}
+
+// What the attention kernels take beside the batch.
+struct AttnCall {
+    const void* const* q;
+    void* const* out;
+    int q_heads;
+    size_t q_stride, out_stride;     // elements
+    float scale;
+};
+
+Handle* handle_of(ar_handle h);      // nullptr if it is not a handle
+
+bool block_norm_fits(size_t hidden, int dt);
+int launch_block_norm(Handle& h, const void* const* in, const ar_block_norm_t& p, void* const* out,
+                      void* residual_out, size_t tokens, size_t hidden, int dt, cudaStream_t s);
+
+struct RopeCall {
+    const void* const* q;            // nullptr: none
+    const void* const* k;
+    const void* const* v;
+    void* const* q_out;
+    int q_heads;
+    size_t q_stride, kv_stride, q_out_stride;
+    const float* cos_sin;
+    size_t max_positions;
+    int rot_dim, interleaved;
+};
+int launch_rope_append(KvCache& kv, const ar_batch_t& b, const RopeCall& c, cudaStream_t s);
+
+size_t attention_decode_partial_floats(const Handle& h, int head_dim);
+size_t attention_decode_counters(const Handle& h);
+int launch_attention_decode(KvCache& kv, const ar_batch_t& b, const AttnCall& c, int window, cudaStream_t s);
+
+}  // namespace argb

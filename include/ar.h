@@ -60,6 +60,7 @@ extern "C" {
 
 typedef struct CUstream_st* ar_stream_t; /* the same type as cudaStream_t */
 typedef struct ar_ctx* ar_handle;        /* opaque */
+typedef struct ar_kv_ctx* ar_kv;         /* opaque: the ranks' paged caches (ar_kv_create) */
 
 typedef enum { AR_F32 = 0, AR_BF16 = 1, AR_F16 = 2 } ar_dtype;
 
@@ -70,8 +71,10 @@ enum {
     AR_ERR_TOO_LARGE = -3,    /* count x element size > max_bytes */
     AR_ERR_CUDA = -4,         /* a CUDA runtime call or a launch failed */
     AR_ERR_FLAG_TIMEOUT = -5, /* an LL/LL128 line never showed the expected flag */
-    AR_ERR_WAIT_TIMEOUT = -6  /* a kernel's bounded wait for its own bulk copies, or the
+    AR_ERR_WAIT_TIMEOUT = -6, /* a kernel's bounded wait for its own bulk copies, or the
                                  persistent ring's wait for a peer's acknowledgement, ran out */
+    AR_ERR_INDEX = -7         /* a page number, length, token range or table row that a kernel read
+                                 from device memory is out of range (ar_batch_t) */
 };
 
 /* Which call an ar_traffic_t describes. */
@@ -95,7 +98,11 @@ typedef enum {
     AR_OP_RING_CLUSTER = 16,
     AR_OP_TREE_FUSED = 17,
     AR_OP_RING_FUSED = 18,
-    AR_OP_RING_ROUNDED_FUSED = 19
+    AR_OP_RING_ROUNDED_FUSED = 19,
+    /* not collectives of a count of elements: ar_traffic reports them, ar_plan does not */
+    AR_OP_ALLREDUCE_BLOCK_NORM = 20,
+    AR_OP_ROPE_APPEND = 21,
+    AR_OP_PAGED_ATTENTION = 22
 } ar_op;
 
 /* Traffic of one call.
@@ -125,7 +132,7 @@ typedef struct {
 
 /* The sticky device-side error of a handle. */
 typedef struct {
-    int code;                /* AR_OK, AR_ERR_FLAG_TIMEOUT or AR_ERR_WAIT_TIMEOUT */
+    int code;                /* AR_OK, AR_ERR_FLAG_TIMEOUT, AR_ERR_WAIT_TIMEOUT or AR_ERR_INDEX */
     int rank;                /* rank whose line lacked the flag (-1: none) */
     uint64_t line;           /* index of the first line found without its flag */
     uint64_t lines_skipped;  /* lines left unconsumed (their outputs untouched) */
@@ -195,7 +202,11 @@ typedef enum {
     AR_K_TREE_FUSED = 20,           /* ar_tree_fused (all levels) */
     AR_K_RING_FUSED = 21,           /* ar_ring_fused (all steps) */
     AR_K_RING_ROUNDED_FUSED = 22,   /* ar_ring_rounded_fused (all steps) */
-    AR_K_TWO_SHOT = 23              /* ar_two_shot in one launch (both phases) */
+    AR_K_TWO_SHOT = 23,             /* ar_two_shot in one launch (both phases) */
+    AR_K_ALLREDUCE_BLOCK_NORM = 24,
+    AR_K_ROPE_APPEND = 25,
+    AR_K_ATTENTION_DECODE = 26,     /* ar_paged_attention, few rows per kv head */
+    AR_K_ATTENTION_CHUNK = 27       /* ar_paged_attention, chunks of tokens */
 } ar_kernel;
 
 /* One timing record: `launches` consecutive launches of one kernel within
@@ -449,6 +460,128 @@ int ar_allreduce_rmsnorm(ar_handle h, const void* const* in, const void* residua
                          void* const* norm_out, void* residual_out, size_t tokens, size_t hidden, ar_dtype dt,
                          ar_stream_t stream);
 
+/* ---- all-reduce fused with the norms around a block ----------------------------- */
+
+/* The epilogue of ar_allreduce_rmsnorm for layers that also norm a block's
+ * output, gate it and scale the residual (per token row):
+ *   a = sum over the ranks of in[r]               (fp32, rank order)
+ *   b = a / sqrt(mean(a^2) + eps) * post_weight   (post_weight NULL: b = a)
+ *   r = alpha * residual + beta * gate * b        (gate NULL: 1)   -> residual_out
+ *   y = r / sqrt(mean(r^2) + eps) * pre_weight                     -> norm_out[0..n-1]
+ * a, b and r stay fp32 in registers; residual_out and y are each rounded once
+ * to the payload type (y is taken from the unrounded r).
+ *   in, norm_out: host arrays of n_ranks device pointers to [tokens][hidden];
+ *   residual, residual_out: [tokens][hidden] (residual_out may equal residual);
+ *   post_weight, pre_weight: [hidden]; gate: row t at gate + t * gate_stride
+ *   elements (0: one row for every token), all in the payload type.
+ * hidden and gate_stride are whole numbers of 16-byte vectors, hidden at most
+ * 65536; alpha and beta are finite, eps >= 0.  In place (norm_out[r] == in[r])
+ * is allowed; otherwise no output may overlap an input or another output. */
+typedef struct {
+    const void* residual;
+    const void* post_weight; /* or NULL */
+    const void* gate;        /* or NULL */
+    size_t gate_stride;      /* elements between token rows of the gate */
+    const void* pre_weight;
+    float alpha, beta, eps;
+} ar_block_norm_t;
+
+int ar_allreduce_block_norm(ar_handle h, const void* const* in, const ar_block_norm_t* p, void* const* norm_out,
+                            void* residual_out, size_t tokens, size_t hidden, ar_dtype dt, ar_stream_t stream);
+
+/* ---- paged caches of the ranks' kv heads ------------------------------------------- */
+
+/* In tensor parallelism each rank holds kv_heads of the layer's kv heads and
+ * caches their keys and values in pages of page_size tokens; the page table
+ * is one for all ranks.  Element (page, head, slot, d) of a rank's K (or V) is
+ * at  page * page_stride + head * head_stride + slot * token_stride + d
+ * elements of k[r] (v[r]), so both [page][head][slot][d] and
+ * [page][slot][head][d] orders, and caches that keep K and V in one
+ * allocation, are described by the strides. */
+typedef struct {
+    int dtype;           /* AR_BF16 or AR_F16 */
+    int kv_heads;        /* per rank, 1..1024 */
+    int head_dim;        /* 64 or 128 */
+    int page_size;       /* tokens per page: 16, 32, 64 or 128 */
+    size_t pages;        /* pages of each rank's cache, 1..2^31-1 */
+    size_t page_stride;  /* elements, each a multiple of 8 */
+    size_t head_stride;
+    size_t token_stride;
+} ar_kv_desc_t;
+
+/* Register the n_ranks caches of a handle: k and v are host arrays of n_ranks
+ * device pointers (16-byte aligned; the caller keeps the memory).  Builds the
+ * copies' descriptors and allocates the attention's workspace (partial results
+ * of rows whose keys are split over several CTAs, about 85 MB) once; no later
+ * call allocates.  Calls on one ar_kv share that workspace: order them on one
+ * stream or with events.  Destroy it before its handle.  *out is set only on
+ * AR_OK. */
+int ar_kv_create(ar_handle h, const ar_kv_desc_t* desc, void* const* k, void* const* v, ar_kv* out);
+
+/* Synchronize the device, then free the registration (not the caches). */
+int ar_kv_destroy(ar_kv kv);
+
+/* A step's new tokens, packed one sequence after the other.  q_start, kv_len
+ * and page_table are DEVICE arrays, so a captured CUDA graph replays with
+ * whatever lengths they hold by then.
+ *   new tokens of sequence s: rows q_start[s] .. q_start[s+1] - 1 of the packed
+ *     tensors; q_start[0] = 0, q_start[seqs] = tokens, never decreasing;
+ *   kv_len[s]: its tokens in the cache including these; new token i has
+ *     position kv_len[s] - (q_start[s+1] - q_start[s]) + i;
+ *   page_table[s * table_stride + j]: its page for positions j * page_size ...
+ * Entries past the last page that a call needs are not read.  A sequence whose
+ * range, length or pages are out of range reaches no memory through them: the
+ * call leaves that token (append) or treats that sequence as empty or that page
+ * as absent (attention: its rows are unspecified) and the handle's status
+ * reads AR_ERR_INDEX. */
+typedef struct {
+    size_t tokens;             /* new tokens in all, at most 2^30 */
+    int seqs;
+    int max_new;               /* most new tokens of one sequence: chooses the kernel, never the result */
+    const int32_t* q_start;    /* [seqs + 1] */
+    const int32_t* kv_len;     /* [seqs] */
+    const int32_t* page_table; /* [seqs][table_stride] */
+    size_t table_stride;       /* pages per sequence, at most 2^27 */
+} ar_batch_t;
+
+/* Rotate the new tokens' queries and keys by their positions, write the
+ * queries to q_out and append keys and values to the caches, in one launch
+ * for all ranks.  With R = rot_dim (0, or a multiple of 16 up to head_dim) and
+ * c, s = cos_sin[position][d], cos_sin[position][R/2 + d] (fp32, device,
+ * [max_positions][R]), for d in 0 .. R/2 - 1:
+ *   (x1, x2) -> (x1 c - x2 s, x2 c + x1 s)
+ * of the pair (x[d], x[d + R/2]), or (x[2d], x[2d+1]) if `interleaved`; the
+ * dimensions from R on, and the values, are copied.  fp32, rounded once.
+ *   q, k, v, q_out: host arrays of n_ranks device pointers to rows of
+ *   q_heads (kv_heads) heads of head_dim, q_stride / kv_stride / q_out_stride
+ *   elements apart (multiples of 8), 16-byte aligned: slices of one packed
+ *   projection are fine.  q and q_out may both be NULL (keys and values only)
+ *   and q_out[r] may equal q[r] with equal strides; no other output may
+ *   overlap an input.
+ * A token whose position is not in 0 .. max_positions - 1 (when R > 0), or
+ * whose page is out of range, is left out and sets AR_ERR_INDEX. */
+int ar_rope_append(ar_kv kv, const ar_batch_t* batch, const void* const* q, const void* const* k,
+                   const void* const* v, void* const* q_out, int q_heads, size_t q_stride, size_t kv_stride,
+                   size_t q_out_stride, const float* cos_sin, size_t max_positions, int rot_dim, int interleaved,
+                   ar_stream_t stream);
+
+/* Causal attention of the new tokens over the caches, one launch for all
+ * ranks: the token at position p attends to the keys at positions j <= p, and
+ * j > p - window if window > 0, of its sequence:
+ *   out = sum_j softmax_j(scale * q . k_j) v_j
+ * with query head h on kv head h / (q_heads / kv_heads).  A token that sees no
+ * key (position < 0) gets 0.  q and out: host arrays of n_ranks device pointers
+ * to rows of q_heads heads of head_dim, q_stride / out_stride elements apart
+ * (multiples of 8), 16-byte aligned, not overlapping.  The caches already hold
+ * the new tokens (ar_rope_append); cache slots at or past kv_len, and before
+ * the window of a sequence's first new token, may hold anything, NaN included.
+ * A non-finite value within them may reach every row of the sequence.
+ * Scores, softmax statistics and sums are fp32; the probabilities are rounded
+ * to the cache's type before they meet the values, the output once at the end.
+ * q_heads is a multiple of kv_heads, at most 64 times it; scale is finite and > 0. */
+int ar_paged_attention(ar_kv kv, const ar_batch_t* batch, const void* const* q, void* const* out, int q_heads,
+                       size_t q_stride, size_t out_stride, float scale, int window, ar_stream_t stream);
+
 /* ---- size-based selection --------------------------------------------------- */
 
 enum {
@@ -568,6 +701,22 @@ int ar_plan(int op, int n_ranks, size_t count, ar_dtype dt, ar_traffic_t* t);
  * compared, never dereferenced.  For the LL ops dt must be AR_F32. */
 int ar_check_args(int op, int n_ranks, size_t max_bytes, const void* const* in,
                   void* const* out, size_t count, ar_dtype dt);
+
+/* Host only, no GPU needed: the codes that ar_allreduce_block_norm,
+ * ar_kv_create, ar_rope_append and ar_paged_attention would return for these
+ * arguments before launching anything (desc: as given to ar_kv_create).
+ * Pointers are compared, never dereferenced, the batch's device arrays among
+ * them. */
+int ar_check_block_norm(int n_ranks, size_t max_bytes, const void* const* in, const ar_block_norm_t* p,
+                        void* const* norm_out, void* residual_out, size_t tokens, size_t hidden, ar_dtype dt);
+int ar_check_kv(int n_ranks, const ar_kv_desc_t* desc, void* const* k, void* const* v);
+int ar_check_rope_append(int n_ranks, const ar_kv_desc_t* desc, const ar_batch_t* batch, const void* const* q,
+                         const void* const* k, const void* const* v, void* const* q_out, int q_heads, size_t q_stride,
+                         size_t kv_stride, size_t q_out_stride, const float* cos_sin, size_t max_positions,
+                         int rot_dim, int interleaved);
+int ar_check_paged_attention(int n_ranks, const ar_kv_desc_t* desc, const ar_batch_t* batch, const void* const* q,
+                             void* const* out, int q_heads, size_t q_stride, size_t out_stride, float scale,
+                             int window);
 
 /* Static text for a return code. */
 const char* ar_strerror(int code);
