@@ -1,0 +1,629 @@
+// Paged attention for chunks of new tokens, on the tensor cores (tcgen05).
+//
+// A row tile is two halves of 128 rows (new tokens x the query heads that
+// share a kv head); against it go tiles of 128 keys.  Per key tile and half the
+// tensor cores do 4 x 128 x 128 x D flops (1024 cycles for both halves at D =
+// 128 and 8192 flops a cycle each way), and the softmax of a half 128 x 128
+// exponentials, so the two halves alternate: while one half's softmax runs on
+// four warps, the tensor cores do the other half's products.
+//
+//   warps 0-3, 4-7  softmax of half 0, 1: thread = row.  Scores come from tensor
+//                   memory, probabilities go back over them (16 bits, A operand
+//                   of the second product), statistics stay in registers
+//   warp 8          one thread issues S = Q K^T and O += P V
+//   warp 9          tensor copies of K and V tiles (pages) into a ring of stages
+//   warps 10, 11    none: with them the last four warps can hand registers to the
+//                   softmax warps, whose threads hold a row of 128 scores
+//
+// Tensor memory (512 columns): S/P of both halves, O of both halves.  Products
+// run in the order they are issued, and a half's S of tile j + 1 is issued
+// after its P V of tile j: when a softmax warp sees S of j + 1, O holds
+// everything up to j and nothing touches it until the warp hands over P, so it
+// may rescale O in place without another wait.
+//
+// Softmax in one pass, base 2, as in the decode kernel: the reference m moves only
+// when a row's maximum passes it by more than 8, so O is rescaled a few times at
+// the start of a row and hardly ever later.
+//
+// Split of the keys over CTAs and the join of the parts: as in the decode
+// kernel (split_work), a half joining its own 128 rows.
+#include "paged.cuh"
+#include "tmem.cuh"
+
+namespace argb {
+namespace {
+
+constexpr int kKeys = 128;
+constexpr int kHalf = kAttnTileRows;        // rows of a half
+constexpr int kTh = 384;
+// Registers a thread: 384 x 168 at launch = 256 x 208 + 128 x 88.
+constexpr int kSoftmaxRegs = 208, kOtherRegs = 88;
+constexpr float kSlack = 8.0f;
+
+template <int D> constexpr int kTileBytes = kKeys * D * 2;    // of K, of V, and of a half's Q
+template <int D> constexpr int kStages = D == 128 ? 5 : 10;
+template <int D> constexpr int kPartFloats = 2 * kHalf * (D + 2);
+
+struct ChunkShared {
+    uint64_t full[10], empty[10];
+    uint64_t q_full[2], s_full[2], p_full[2], o_full[2], drained;
+    SplitShared split;
+    uint32_t tmem;
+    int gave_up, last[2];
+};
+static_assert(sizeof(ChunkShared) <= 1024, "fits beside the tiles");
+
+template <int D> constexpr int kSmem = (2 + kStages<D>) * kTileBytes<D> + 1024;
+
+struct ChunkArgs {
+    const void* q[kMaxRanks];
+    void* out[kMaxRanks];
+    const CUtensorMap* maps;
+    float* partial;
+    unsigned* arrived;
+    size_t q_stride, out_stride;
+    float scale_log2;
+    int n, kv_heads, group;                  // query heads per kv head
+    int half_tokens;                         // new tokens of a half: 128 / group
+    int box_tokens, min_units;
+};
+
+// One half's share of a segment.
+struct HalfTile {
+    int tok0, rows;    // first new token, rows
+    int tiles;         // key tiles of this CTA that it sees any key of
+};
+
+__device__ __forceinline__ HalfTile half_tile(const ChunkArgs& a, const Segment& seg, int h)
+{
+    HalfTile x;
+    x.tok0 = (2 * seg.t + h) * a.half_tokens;
+    const int tokens = max(min(a.half_tokens, seg.q.nq - x.tok0), 0);
+    x.rows = tokens * a.group;
+    const int key_hi = tokens ? max(seg.q.c0 + x.tok0 + tokens, 0) : 0;
+    x.tiles = max(min((key_hi + kKeys - 1) / kKeys, seg.j1) - seg.j0, 0);
+    return x;
+}
+
+__device__ __forceinline__ void half_sync(int h)
+{
+    if (h == 0)
+        asm volatile("bar.sync 1, %0;" ::"n"(kHalf) : "memory");
+    else
+        asm volatile("bar.sync 2, %0;" ::"n"(kHalf) : "memory");
+}
+
+template <int D>
+__device__ void produce(const ChunkArgs& a, const BatchArgs& b, const Cursor& cur, uint8_t* stages, ChunkShared* sh,
+                        DevStatus* st)
+{
+    const int lane = threadIdx.x & 31;
+    const int per_tile = kKeys / a.box_tokens;          // boxes of a tile along the keys: 2, 4 or 8
+    const int box = lane % per_tile, panel = lane / per_tile;
+    const bool mine = panel < D / 64;
+    Walk<kKeys> walk(cur);
+    Segment seg;
+    int stage = 0;
+    uint32_t phase = 0, issued = 0;
+    bool ok = true;
+    while (ok && walk.next(b, 2 * a.half_tokens, seg, st)) {
+        const int tiles = max(half_tile(a, seg, 0).tiles, half_tile(a, seg, 1).tiles);
+        const int kv_head = seg.head % a.kv_heads, rank = seg.head / a.kv_heads;
+        const int32_t* row = b.table + (size_t)seg.s * b.table_stride;
+        for (int j = seg.j0; ok && j < seg.j0 + tiles; ++j) {
+            const int key = j * kKeys + box * a.box_tokens;
+            bool copy = mine && key < seg.span.key_hi && key + a.box_tokens > seg.span.key_lo;
+            int page = 0;
+            if (copy) {
+                page = row[key >> b.page_shift];
+                if (page < 0 || page >= b.pages) {
+                    report_index(st);
+                    copy = false;
+                }
+            }
+            const uint32_t bytes = __popc(__ballot_sync(0xffffffffu, copy)) * a.box_tokens * 128u;
+            for (int v = 0; v < 2; ++v) {   // K, then V
+                if (issued >= (uint32_t)kStages<D>)
+                    ok = wait_or_give_up(&sh->empty[stage], phase ^ 1, &sh->gave_up, st);
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok) break;
+                if (lane == 0) mbar_arrive_expect_tx(&sh->full[stage], bytes);
+                __syncwarp();
+                if (copy)
+                    page_copy(stages + (size_t)stage * kTileBytes<D> + panel * (kKeys * 128) + box * a.box_tokens * 128,
+                              a.maps + (v ? a.n : 0) + rank, panel * 64, key & ((1 << b.page_shift) - 1), kv_head, page,
+                              &sh->full[stage]);
+                ++issued;
+                if (++stage == kStages<D>) {
+                    stage = 0;
+                    phase ^= 1;
+                }
+            }
+        }
+    }
+    // after a wait that ran out the copies in flight still land in this CTA's shared memory
+    if (!ok)
+        for (uint32_t k = 0; k < issued && k < (uint32_t)kStages<D>; ++k) {
+            stage = stage == 0 ? kStages<D> - 1 : stage - 1;
+            if (stage == kStages<D> - 1) phase ^= 1;
+            wait_a_second(&sh->full[stage], phase, nullptr);
+        }
+}
+
+template <int DT, int D>
+__device__ void issue(const ChunkArgs& a, const BatchArgs& b, const Cursor& cur, uint8_t* q_tiles, uint8_t* stages,
+                      ChunkShared* sh, DevStatus* st)
+{
+    constexpr uint32_t kScores = mma_shape(DT == AR_BF16, kKeys, false);
+    constexpr uint32_t kValues = mma_shape(DT == AR_BF16, D, true);
+    const int lane = threadIdx.x & 31;
+    const uint32_t tmem = sh->tmem;
+    Walk<kKeys> walk(cur);
+    Segment seg;
+    int stage = 0;                // of the next tile in the ring
+    uint32_t phase = 0;
+    uint32_t q_phase[2] = {0, 0}, p_phase[2] = {0, 0};
+    bool ok = true;
+    auto wait = [&](uint64_t* bar, uint32_t parity) {
+        if (ok) ok = wait_or_give_up(bar, parity, &sh->gave_up, st);
+        ok = __all_sync(0xffffffffu, ok);
+    };
+    auto step = [&](int& s, uint32_t& p) {
+        if (++s == kStages<D>) {
+            s = 0;
+            p ^= 1;
+        }
+    };
+    // S of half h = its Q times the keys in `from`
+    auto scores = [&](int h, int from) {
+        if (lane == 0 && ok) {
+            const uint32_t qa = smem_addr(q_tiles + h * kTileBytes<D>), ka = smem_addr(stages + from * kTileBytes<D>);
+#pragma unroll
+            for (int k = 0; k < D / 16; ++k) {
+                const uint32_t off = (k / 4) * (kKeys * 128) + (k % 4) * 32;
+                mma_ss(tmem + h * kKeys, mma_operand(qa + off, 1024, 16), mma_operand(ka + off, 1024, 16), kScores,
+                       k > 0);
+            }
+            mma_commit(&sh->s_full[h]);
+        }
+        __syncwarp();
+    };
+    while (ok && walk.next(b, 2 * a.half_tokens, seg, st)) {
+        const int n[2] = {half_tile(a, seg, 0).tiles, half_tile(a, seg, 1).tiles};
+        const int tiles = max(n[0], n[1]);
+        if (tiles == 0) continue;
+        wait(&sh->full[stage], phase);
+        for (int h = 0; h < 2; ++h)
+            if (n[h] > 0) {
+                wait(&sh->q_full[h], q_phase[h]);
+                q_phase[h] ^= 1;
+                tmem_after_sync();
+                scores(h, stage);
+            }
+        if (lane == 0 && ok) mma_commit(&sh->empty[stage]);
+        __syncwarp();
+        step(stage, phase);
+        for (int i = 0; ok && i < tiles; ++i) {
+            const int v_stage = stage;
+            const uint32_t v_phase = phase;
+            step(stage, phase);
+            const int k_stage = stage;
+            const uint32_t k_phase = phase;
+            const bool more = i + 1 < tiles;
+            if (more) step(stage, phase);
+            wait(&sh->full[v_stage], v_phase);
+            const int key0 = (seg.j0 + i) * kKeys;
+            if (key0 + kKeys > seg.span.key_hi || key0 < seg.span.key_lo) {
+                // slots of these pages that no row sees may hold anything: their values count as 0
+                const uint32_t base = smem_addr(stages + v_stage * kTileBytes<D>);
+                for (int x = lane; x < kKeys * (D / 8); x += 32) {
+                    const int r = x / (D / 8), c = x % (D / 8);
+                    if (key0 + r >= seg.span.key_hi || key0 + r < seg.span.key_lo) {
+                        const uint32_t at = base + (c >> 3) * (kKeys * 128) + r * 128 + (c & 7) * 16;
+                        asm volatile("st.shared.v4.b32 [%0], {%1,%1,%1,%1};" ::"r"(at), "r"(0) : "memory");
+                    }
+                }
+                fence_proxy_async();
+                __syncwarp();
+            }
+            bool k_here = false;
+            for (int h = 0; h < 2; ++h) {
+                if (i >= n[h]) continue;
+                wait(&sh->p_full[h], p_phase[h]);
+                p_phase[h] ^= 1;
+                tmem_after_sync();
+                if (lane == 0 && ok) {
+                    const uint32_t va = smem_addr(stages + v_stage * kTileBytes<D>);
+#pragma unroll
+                    for (int k = 0; k < kKeys / 16; ++k)
+                        mma_ts(tmem + 2 * kKeys + h * D, tmem + h * kKeys + 8 * k,
+                               mma_operand(va + k * 2048, 1024, kKeys * 128), kValues, i > 0 || k > 0);
+                    if (i + 1 == n[h]) mma_commit(&sh->o_full[h]);
+                }
+                __syncwarp();
+                if (i + 1 < n[h]) {
+                    if (!k_here) {
+                        wait(&sh->full[k_stage], k_phase);
+                        k_here = true;
+                    }
+                    scores(h, k_stage);
+                }
+            }
+            if (lane == 0 && ok) {
+                mma_commit(&sh->empty[v_stage]);
+                if (more) mma_commit(&sh->empty[k_stage]);
+            }
+            __syncwarp();
+        }
+    }
+    // nothing that was issued may still run when the tensor memory is freed
+    if (lane == 0) mma_commit(&sh->drained);
+    __syncwarp();
+    if (!wait_a_second(&sh->drained, 0, nullptr)) report_wait_timeout(st);
+}
+
+__device__ __forceinline__ uint64_t pack2(float x, float y)
+{
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
+    return r;
+}
+__device__ __forceinline__ void unpack2(uint64_t r, float& x, float& y)
+{
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(r));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c)
+{
+    uint64_t d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b)
+{
+    uint64_t d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+
+template <int DT, int D>
+__device__ void soften(const ChunkArgs& a, const BatchArgs& b, const Cursor& cur, uint8_t* q_tiles, ChunkShared* sh,
+                       DevStatus* st)
+{
+    using T = typename Payload<DT>::scalar_t;
+    const int h = threadIdx.x / kHalf, row = threadIdx.x % kHalf, lane = threadIdx.x & 31;
+    const uint32_t lanes = (uint32_t)(row & ~31) << 16;
+    const uint32_t s_at = sh->tmem + lanes + h * kKeys, o_at = sh->tmem + lanes + 2 * kKeys + h * D;
+    uint8_t* q_tile = q_tiles + h * kTileBytes<D>;
+    bool ok = true;
+    uint32_t s_phase = 0, o_phase = 0;
+
+    auto load_q = [&](const Segment& seg, const HalfTile& x) {
+        // 16 threads (8 for D = 64) a row, a row after the other, swizzled as the copies swizzle K
+        if (x.tiles == 0) return;
+        const int kv_head = seg.head % a.kv_heads, rank = seg.head / a.kv_heads;
+        const T* from = static_cast<const T*>(a.q[rank]) + (size_t)kv_head * a.group * D;
+        constexpr int C = D / 8;
+        uint4 v[C];
+#pragma unroll
+        for (int k = 0; k < C; ++k) {
+            const int i = k * kHalf + row, r = i / C, c = i % C;
+            v[k] = make_uint4(0u, 0u, 0u, 0u);
+            if (r < x.rows)
+                v[k] = ld16(from + (size_t)(seg.q.q0 + x.tok0 + r / a.group) * a.q_stride + (size_t)(r % a.group) * D +
+                            8 * c);
+        }
+#pragma unroll
+        for (int k = 0; k < C; ++k) {
+            const int i = k * kHalf + row, r = i / C, c = i % C;
+            const uint32_t at = swizzled(smem_addr(q_tile) + (c >> 3) * (kHalf * 128), r, c & 7);
+            asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(at), "r"(v[k].x), "r"(v[k].y), "r"(v[k].z),
+                         "r"(v[k].w)
+                         : "memory");
+        }
+        fence_proxy_async();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh->q_full[h]);
+    };
+
+    Walk<kKeys> walk(cur);
+    Segment seg, next;
+    HalfTile x;
+    bool have = walk.next(b, 2 * a.half_tokens, seg, st);
+    if (have) {
+        x = half_tile(a, seg, h);
+        load_q(seg, x);
+    }
+    while (have) {
+        // keys this row sees, and the range that every row of the half sees
+        const bool there = row < x.rows;
+        const int limit = there ? seg.q.c0 + x.tok0 + row / a.group + 1 : 0;
+        const int lower = b.window > 0 ? limit - b.window : 0;
+        const int all_hi = seg.q.c0 + x.tok0 + 1;
+        const int all_lo = b.window > 0 ? seg.q.c0 + x.tok0 + x.rows / a.group - b.window : 0;
+        float m = -INFINITY;
+        uint64_t l2[2] = {0ull, 0ull};
+        float l_scale_acc = 0.0f;   // sums before the last move of m
+        for (int i = 0; i < x.tiles; ++i) {
+            if (ok) ok = wait_or_give_up(&sh->s_full[h], s_phase, &sh->gave_up, st);
+            ok = __all_sync(0xffffffffu, ok);
+            s_phase ^= 1;
+            if (!ok) break;
+            tmem_after_sync();
+            float s[kKeys];
+#pragma unroll
+            for (int k = 0; k < kKeys; k += 32) tmem_ld32(s + k, s_at + k);
+            tmem_wait_ld();
+            const int key0 = (seg.j0 + i) * kKeys;
+            if (key0 + kKeys > all_hi || key0 < all_lo) {
+                const int hi = limit - key0, lo = lower - key0;
+#pragma unroll
+                for (int k = 0; k < kKeys; ++k)
+                    if (k >= hi || k < lo) s[k] = -INFINITY;
+            }
+            float mx[4] = {s[0], s[1], s[2], s[3]};
+#pragma unroll
+            for (int k = 4; k < kKeys; k += 4) {
+                mx[0] = fmaxf(mx[0], s[k]);
+                mx[1] = fmaxf(mx[1], s[k + 1]);
+                mx[2] = fmaxf(mx[2], s[k + 2]);
+                mx[3] = fmaxf(mx[3], s[k + 3]);
+            }
+            const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * a.scale_log2;
+            const bool move = top > m + kSlack;
+            if (__any_sync(0xffffffffu, move)) {
+                const float to = move ? top : m;
+                const float f = m == -INFINITY ? 0.0f : ex2(m - to);
+                m = to;
+                float p, q, u, v;
+                unpack2(l2[0], p, q);
+                unpack2(l2[1], u, v);
+                l_scale_acc = (l_scale_acc + ((p + q) + (u + v))) * f;
+                l2[0] = l2[1] = 0ull;
+                if (i > 0) {
+#pragma unroll
+                    for (int k = 0; k < D; k += 32) {
+                        float o[32];
+                        tmem_ld32(o, o_at + k);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) o[e] *= f;
+                        tmem_st32(o_at + k, reinterpret_cast<const uint32_t*>(o));
+                    }
+                }
+            }
+            const float ref = m == -INFINITY ? 0.0f : m;
+            const uint64_t sc = pack2(a.scale_log2, a.scale_log2), off = pack2(-ref, -ref);
+#pragma unroll
+            for (int g = 0; g < 2; ++g) {
+                uint32_t pw[32];
+#pragma unroll
+                for (int k = 0; k < 32; ++k) {
+                    float y[2];
+                    const int e = 64 * g + 2 * k;
+                    unpack2(fma2(pack2(s[e], s[e + 1]), sc, off), y[0], y[1]);
+                    y[0] = ex2(y[0]);
+                    y[1] = ex2(y[1]);
+                    l2[k & 1] = add2(l2[k & 1], pack2(y[0], y[1]));
+                    // rounded to the cache's type: the product's operand (at most half a step of it each)
+                    pw[k] = Payload<DT>::narrow(y);
+                }
+                tmem_st32(s_at + 32 * g, pw);
+            }
+            tmem_wait_st();
+            tmem_before_sync();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sh->p_full[h]);
+        }
+        const HalfTile done = x;
+        const bool more = walk.next(b, 2 * a.half_tokens, next, st);
+        if (more) {
+            x = half_tile(a, next, h);
+            if (ok) load_q(next, x);
+        }
+
+        // the row's sum and result
+        float p, q, u, v;
+        unpack2(l2[0], p, q);
+        unpack2(l2[1], u, v);
+        const float l = l_scale_acc + ((p + q) + (u + v));
+        if (done.tiles > 0) {
+            if (ok) ok = wait_or_give_up(&sh->o_full[h], o_phase, &sh->gave_up, st);
+            ok = __all_sync(0xffffffffu, ok);
+            o_phase ^= 1;
+            tmem_after_sync();
+        }
+        const int kv_head = seg.head % a.kv_heads, rank = seg.head / a.kv_heads;
+        T* to = static_cast<T*>(a.out[rank]) + (size_t)(seg.q.q0 + done.tok0 + row / a.group) * a.out_stride +
+                (size_t)(kv_head * a.group + row % a.group) * D;
+        auto store32 = [&](const float* o, int k) {
+#pragma unroll
+            for (int e = 0; e < 32; e += 8) {
+                float w[8];
+#pragma unroll
+                for (int y = 0; y < 8; ++y) w[y] = o[e + y];
+                uint4 r;
+                r.x = Payload<DT>::narrow(w);
+                r.y = Payload<DT>::narrow(w + 2);
+                r.z = Payload<DT>::narrow(w + 4);
+                r.w = Payload<DT>::narrow(w + 6);
+                st16_next(to + k + e, r);
+            }
+        };
+        if (seg.whole) {
+            const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+#pragma unroll
+            for (int k = 0; k < D; k += 32) {
+                float o[32];
+                if (done.tiles > 0 && ok) {
+                    tmem_ld32(o, o_at + k);
+                    tmem_wait_ld();
+                }
+#pragma unroll
+                for (int e = 0; e < 32; ++e) o[e] = done.tiles > 0 ? o[e] * inv : 0.0f;
+                if (row < done.rows && ok) store32(o, k);
+            }
+        } else {
+            // column after column, so that the warp's rows are consecutive words
+            float* part = a.partial + (size_t)seg.slot * kPartFloats<D> + h * (kHalf * (D + 2));
+            if (done.tiles > 0 && ok)
+#pragma unroll
+                for (int k = 0; k < D; k += 32) {
+                    float o[32];
+                    tmem_ld32(o, o_at + k);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) __stcg(part + (k + e) * kHalf + row, o[e]);
+                }
+            __stcg(part + D * kHalf + row, m);
+            __stcg(part + (D + 1) * kHalf + row, l);
+            __threadfence();
+            half_sync(h);
+            if (row == 0) {
+                unsigned* count = &a.arrived[2 * seg.first_cta + h];
+                sh->last[h] = atomicAdd(count, 1u) + 1 == seg.parts;
+                if (sh->last[h]) *count = 0;   // for the next call
+            }
+            half_sync(h);
+            if (sh->last[h]) {
+                __threadfence();
+                auto part_of = [&](unsigned k) {
+                    return a.partial + (size_t)part_slot(seg.first_cta, k) * kPartFloats<D> + h * (kHalf * (D + 2));
+                };
+                float top = -INFINITY, sum = 0.0f;
+                for (unsigned k = 0; k < seg.parts; ++k) top = fmaxf(top, __ldcg(part_of(k) + D * kHalf + row));
+                for (unsigned k = 0; k < seg.parts; ++k) {
+                    const float pm = __ldcg(part_of(k) + D * kHalf + row);
+                    if (pm != -INFINITY) sum = fmaf(__ldcg(part_of(k) + (D + 1) * kHalf + row), ex2(pm - top), sum);
+                }
+                const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+#pragma unroll 1
+                for (int k = 0; k < D; k += 32) {
+                    float o[32];
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) o[e] = 0.0f;
+                    for (unsigned y = 0; y < seg.parts; ++y) {
+                        const float* from = part_of(y);
+                        const float pm = __ldcg(from + D * kHalf + row);
+                        if (pm == -INFINITY) continue;   // a part that saw nothing wrote no columns
+                        const float w = ex2(pm - top);
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) o[e] = fmaf(__ldcg(from + (k + e) * kHalf + row), w, o[e]);
+                    }
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) o[e] *= inv;
+                    if (row < done.rows) store32(o, k);
+                }
+            }
+        }
+        __syncwarp();
+        have = more;
+        seg = next;
+    }
+}
+
+template <int DT, int D>
+__global__ void __launch_bounds__(kTh, 1)
+attention_chunk_kernel(const __grid_constant__ ChunkArgs a, const BatchArgs b, DevStatus* st)
+{
+    extern __shared__ __align__(1024) uint8_t smem[];
+    uint8_t* q_tiles = smem;
+    uint8_t* stages = smem + 2 * kTileBytes<D>;
+    ChunkShared* sh = reinterpret_cast<ChunkShared*>(stages + kStages<D> * kTileBytes<D>);
+    const int warp = threadIdx.x / 32;
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < kStages<D>; ++i) {
+            mbar_init(&sh->full[i], 1);
+            mbar_init(&sh->empty[i], 1);
+        }
+        for (int h = 0; h < 2; ++h) {
+            mbar_init(&sh->q_full[h], kHalf / 32);
+            mbar_init(&sh->s_full[h], 1);
+            mbar_init(&sh->p_full[h], kHalf / 32);
+            mbar_init(&sh->o_full[h], 1);
+        }
+        mbar_init(&sh->drained, 1);
+        mbar_init_fence();
+        sh->gave_up = 0;
+    }
+    pdl_acquire();
+    const Cursor cur = split_work<kKeys, kTh>(b, 2 * a.half_tokens, a.n * a.kv_heads, a.min_units, &sh->split, st);
+    if (cur.g >= cur.end) {
+        pdl_release();
+        return;
+    }
+    if (warp == 8) tmem_alloc(&sh->tmem, 512);
+    tmem_before_sync();
+    __syncthreads();
+    tmem_after_sync();
+    if (warp < 8) {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
+        soften<DT, D>(a, b, cur, q_tiles, sh, st);
+    } else {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
+        if (warp == 8)
+            issue<DT, D>(a, b, cur, q_tiles, stages, sh, st);
+        else if (warp == 9)
+            produce<D>(a, b, cur, stages, sh, st);
+    }
+    pdl_release();
+    tmem_before_sync();
+    __syncthreads();
+    if (warp == 8) {
+        tmem_after_sync();
+        tmem_free(sh->tmem, 512);
+    }
+}
+
+}  // namespace
+
+size_t attention_chunk_partial_floats(const Handle& h, int head_dim)
+{
+    return (size_t)(2 * h.sm_count) * (size_t)(2 * kHalf * (head_dim + 2));
+}
+
+size_t attention_chunk_counters(const Handle& h) { return (size_t)(2 * h.sm_count); }
+
+int launch_attention_chunk(KvCache& kv, const ar_batch_t& b, const AttnCall& c, int window, cudaStream_t s)
+{
+    Handle& h = *kv.h;
+    ChunkArgs a{};
+    for (int r = 0; r < h.n; ++r) {
+        a.q[r] = c.q[r];
+        a.out[r] = c.out[r];
+    }
+    a.maps = kv.maps;
+    a.partial = kv.partial;
+    a.arrived = kv.arrived;
+    a.q_stride = c.q_stride;
+    a.out_stride = c.out_stride;
+    a.scale_log2 = c.scale * 1.4426950408889634f;
+    a.n = h.n;
+    a.kv_heads = kv.d.kv_heads;
+    a.group = c.q_heads / kv.d.kv_heads;
+    a.half_tokens = kHalf / a.group;
+    a.box_tokens = kv.box_tokens;
+    a.min_units = 4;
+    const uint64_t moved = (uint64_t)h.n * b.tokens * c.q_heads * kv.d.head_dim * 2u * 2u;
+    auto run = [&](auto dtc, auto dc) -> int {
+        constexpr int DT = decltype(dtc)::value, D = decltype(dc)::value;
+        static std::atomic<uint32_t> attr_done{0};
+        if (!once_per_device(attr_done, [&] {
+                return cudaFuncSetAttribute(attention_chunk_kernel<DT, D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                            kSmem<D>) == cudaSuccess;
+            }))
+            return AR_ERR_CUDA;
+        rec_begin(h, s);
+        const cudaError_t e = launch_kernel(h, attention_chunk_kernel<DT, D>, dim3((unsigned)h.sm_count), dim3(kTh),
+                                            kSmem<D>, s, a, batch_args(kv, b, window), h.status);
+        rec_end(h, s, AR_K_ATTENTION_CHUNK, moved);
+        return e == cudaSuccess ? launch_status() : AR_ERR_CUDA;
+    };
+    using BF = std::integral_constant<int, AR_BF16>;
+    using HF = std::integral_constant<int, AR_F16>;
+    using D64 = std::integral_constant<int, 64>;
+    using D128 = std::integral_constant<int, 128>;
+    if (kv.d.dtype == AR_BF16) return kv.d.head_dim == 128 ? run(BF{}, D128{}) : run(BF{}, D64{});
+    return kv.d.head_dim == 128 ? run(HF{}, D128{}) : run(HF{}, D64{});
+}
+
+}  // namespace argb

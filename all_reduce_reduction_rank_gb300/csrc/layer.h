@@ -74,6 +74,9 @@ int launch_rope_append(KvCache& kv, const ar_batch_t& b, const RopeCall& c, cuda
 
 size_t attention_decode_partial_floats(const Handle& h, int head_dim);
 size_t attention_decode_counters(const Handle& h);
+size_t attention_chunk_partial_floats(const Handle& h, int head_dim);
+size_t attention_chunk_counters(const Handle& h);
 int launch_attention_decode(KvCache& kv, const ar_batch_t& b, const AttnCall& c, int window, cudaStream_t s);
+int launch_attention_chunk(KvCache& kv, const ar_batch_t& b, const AttnCall& c, int window, cudaStream_t s);
 
 }  // namespace argb

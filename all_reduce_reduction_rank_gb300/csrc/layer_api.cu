@@ -1,6 +1,7 @@
 // C-ABI entry points of the paged caches, the rotation and append, and the
 // attention (declared in include/ar.h): argument checks and launches.  Host
 // code only; nothing here allocates after ar_kv_create.
+#include <algorithm>
 #include <climits>
 #include <cmath>
 #include <cstring>
@@ -207,8 +208,9 @@ int ar_kv_create(ar_handle hd, const ar_kv_desc_t* d, void* const* k, void* cons
             if (encode((PFN_cuTensorMapEncodeTiled_v12000)fn, &maps[r], *d, kv.box_tokens, k[r]) != CUDA_SUCCESS ||
                 encode((PFN_cuTensorMapEncodeTiled_v12000)fn, &maps[h->n + r], *d, kv.box_tokens, v[r]) != CUDA_SUCCESS)
                 return AR_ERR_INVALID;
-        const size_t floats = attention_decode_partial_floats(*h, d->head_dim);
-        const size_t counters = attention_decode_counters(*h);
+        const size_t floats = std::max(attention_decode_partial_floats(*h, d->head_dim),
+                                       attention_chunk_partial_floats(*h, d->head_dim));
+        const size_t counters = std::max(attention_decode_counters(*h), attention_chunk_counters(*h));
         const size_t map_bytes = 2u * (size_t)h->n * sizeof(CUtensorMap);
         if (cudaMalloc(&kv.maps, map_bytes) != cudaSuccess || cudaMalloc(&kv.partial, floats * 4u) != cudaSuccess ||
             cudaMalloc(&kv.arrived, counters * sizeof(unsigned)) != cudaSuccess ||
@@ -304,8 +306,13 @@ int ar_paged_attention(ar_kv k, const ar_batch_t* b, const void* const* q, void*
     const size_t row = (size_t)kv->d.head_dim * (size_t)q_heads;
     int rc = AR_OK;
     h.timing.op = AR_OP_PAGED_ATTENTION;
+    // rows of a sequence per kv head: the decode kernel's tile holds 16
+    const bool few = (size_t)b->max_new * (size_t)(q_heads / kv->d.kv_heads) <= 16u || b->max_new == 1;
     if (b->tokens)
-        rc = on_device_of(h, [&] { return launch_attention_decode(*kv, *b, c, window, (cudaStream_t)stream); });
+        rc = on_device_of(h, [&] {
+            return few ? launch_attention_decode(*kv, *b, c, window, (cudaStream_t)stream)
+                       : launch_attention_chunk(*kv, *b, c, window, (cudaStream_t)stream);
+        });
     if (rc != AR_OK) return rc;
     const uint64_t moved = 2ull * h.n * b->tokens * row;
     note(h, AR_OP_PAGED_ATTENTION, b->tokens * row, moved, moved, (cudaStream_t)stream);
