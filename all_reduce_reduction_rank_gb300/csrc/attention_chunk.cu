@@ -50,10 +50,14 @@ struct ChunkShared {
     SplitShared split;
     uint32_t tmem;
     int gave_up, last[2];
+    // each softmax warp's place in the run: kept here, so that the loop over the
+    // keys has the registers
+    Walk<kKeys> walk[8];
+    Segment seg[8];
 };
-static_assert(sizeof(ChunkShared) <= 1024, "fits beside the tiles");
+static_assert(sizeof(ChunkShared) <= 3072, "fits beside the tiles");
 
-template <int D> constexpr int kSmem = (2 + kStages<D>) * kTileBytes<D> + 1024;
+template <int D> constexpr int kSmem = (2 + kStages<D>) * kTileBytes<D> + 3072;
 
 struct ChunkArgs {
     const void* q[kMaxRanks];
@@ -300,6 +304,8 @@ __device__ void soften(const ChunkArgs& a, const BatchArgs& b, const Cursor& cur
     auto load_q = [&](const Segment& seg, const HalfTile& x) {
         // 16 threads (8 for D = 64) a row, a row after the other, swizzled as the copies swizzle K
         if (x.tiles == 0) return;
+        int group = a.group;
+        asm volatile("" : "+r"(group));   // the rows' places are computed here, not kept in registers over the loop
         const int kv_head = seg.head % a.kv_heads, rank = seg.head / a.kv_heads;
         const T* from = static_cast<const T*>(a.q[rank]) + (size_t)kv_head * a.group * D;
         constexpr int C = D / 8;
@@ -309,7 +315,7 @@ __device__ void soften(const ChunkArgs& a, const BatchArgs& b, const Cursor& cur
             const int i = k * kHalf + row, r = i / C, c = i % C;
             v[k] = make_uint4(0u, 0u, 0u, 0u);
             if (r < x.rows)
-                v[k] = ld16(from + (size_t)(seg.q.q0 + x.tok0 + r / a.group) * a.q_stride + (size_t)(r % a.group) * D +
+                v[k] = ld16(from + (size_t)(seg.q.q0 + x.tok0 + r / group) * a.q_stride + (size_t)(r % group) * D +
                             8 * c);
         }
 #pragma unroll
@@ -325,25 +331,36 @@ __device__ void soften(const ChunkArgs& a, const BatchArgs& b, const Cursor& cur
         if (lane == 0) mbar_arrive(&sh->q_full[h]);
     };
 
-    Walk<kKeys> walk(cur);
-    Segment seg, next;
+    const int warp = threadIdx.x / 32;
     HalfTile x;
-    bool have = walk.next(b, 2 * a.half_tokens, seg, st);
-    if (have) {
-        x = half_tile(a, seg, h);
-        load_q(seg, x);
-    }
+    // the next segment, from and to shared memory
+    auto advance = [&](Walk<kKeys> walk) {
+        Segment seg;
+        const bool more = walk.next(b, 2 * a.half_tokens, seg, st);
+        __syncwarp();
+        if (lane == 0) {
+            sh->walk[warp] = walk;
+            sh->seg[warp] = seg;
+        }
+        __syncwarp();
+        if (more) {
+            x = half_tile(a, seg, h);
+            if (ok) load_q(seg, x);
+        }
+        return more;
+    };
+    bool have = advance(Walk<kKeys>(cur));
     while (have) {
         // keys this row sees, and the range that every row of the half sees
-        const bool there = row < x.rows;
-        const int limit = there ? seg.q.c0 + x.tok0 + row / a.group + 1 : 0;
+        const int first = sh->seg[warp].q.c0 + x.tok0, j0 = sh->seg[warp].j0, tiles = x.tiles;
+        const int limit = row < x.rows ? first + row / a.group + 1 : 0;
         const int lower = b.window > 0 ? limit - b.window : 0;
-        const int all_hi = seg.q.c0 + x.tok0 + 1;
-        const int all_lo = b.window > 0 ? seg.q.c0 + x.tok0 + x.rows / a.group - b.window : 0;
+        const int all_hi = first + 1;
+        const int all_lo = b.window > 0 ? first + x.rows / a.group - b.window : 0;
         float m = -INFINITY;
         uint64_t l2[2] = {0ull, 0ull};
-        float l_scale_acc = 0.0f;   // sums before the last move of m
-        for (int i = 0; i < x.tiles; ++i) {
+        float l_before = 0.0f;   // the sum before the last move of m
+        for (int i = 0; i < tiles; ++i) {
             if (ok) ok = wait_or_give_up(&sh->s_full[h], s_phase, &sh->gave_up, st);
             ok = __all_sync(0xffffffffu, ok);
             s_phase ^= 1;
@@ -353,7 +370,7 @@ __device__ void soften(const ChunkArgs& a, const BatchArgs& b, const Cursor& cur
 #pragma unroll
             for (int k = 0; k < kKeys; k += 32) tmem_ld32(s + k, s_at + k);
             tmem_wait_ld();
-            const int key0 = (seg.j0 + i) * kKeys;
+            const int key0 = (j0 + i) * kKeys;
             if (key0 + kKeys > all_hi || key0 < all_lo) {
                 const int hi = limit - key0, lo = lower - key0;
 #pragma unroll
@@ -370,26 +387,17 @@ __device__ void soften(const ChunkArgs& a, const BatchArgs& b, const Cursor& cur
             }
             const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * a.scale_log2;
             const bool move = top > m + kSlack;
-            if (__any_sync(0xffffffffu, move)) {
+            const bool rescale = __any_sync(0xffffffffu, move);
+            float f = 1.0f;
+            if (rescale) {
                 const float to = move ? top : m;
-                const float f = m == -INFINITY ? 0.0f : ex2(m - to);
+                f = m == -INFINITY ? 0.0f : ex2(m - to);
                 m = to;
                 float p, q, u, v;
                 unpack2(l2[0], p, q);
                 unpack2(l2[1], u, v);
-                l_scale_acc = (l_scale_acc + ((p + q) + (u + v))) * f;
+                l_before = (l_before + ((p + q) + (u + v))) * f;
                 l2[0] = l2[1] = 0ull;
-                if (i > 0) {
-#pragma unroll
-                    for (int k = 0; k < D; k += 32) {
-                        float o[32];
-                        tmem_ld32(o, o_at + k);
-                        tmem_wait_ld();
-#pragma unroll
-                        for (int e = 0; e < 32; ++e) o[e] *= f;
-                        tmem_st32(o_at + k, reinterpret_cast<const uint32_t*>(o));
-                    }
-                }
             }
             const float ref = m == -INFINITY ? 0.0f : m;
             const uint64_t sc = pack2(a.scale_log2, a.scale_log2), off = pack2(-ref, -ref);
@@ -409,23 +417,31 @@ __device__ void soften(const ChunkArgs& a, const BatchArgs& b, const Cursor& cur
                 }
                 tmem_st32(s_at + 32 * g, pw);
             }
+            if (rescale && i > 0) {   // after the scores have left the registers
+#pragma unroll 1
+                for (int k = 0; k < D; k += 32) {
+                    float o[32];
+                    tmem_ld32(o, o_at + k);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) o[e] *= f;
+                    tmem_st32(o_at + k, reinterpret_cast<const uint32_t*>(o));
+                }
+            }
             tmem_wait_st();
             tmem_before_sync();
             __syncwarp();
             if (lane == 0) mbar_arrive(&sh->p_full[h]);
         }
+        const Segment seg = sh->seg[warp];
         const HalfTile done = x;
-        const bool more = walk.next(b, 2 * a.half_tokens, next, st);
-        if (more) {
-            x = half_tile(a, next, h);
-            if (ok) load_q(next, x);
-        }
+        have = advance(sh->walk[warp]);
 
         // the row's sum and result
         float p, q, u, v;
         unpack2(l2[0], p, q);
         unpack2(l2[1], u, v);
-        const float l = l_scale_acc + ((p + q) + (u + v));
+        const float l = l_before + ((p + q) + (u + v));
         if (done.tiles > 0) {
             if (ok) ok = wait_or_give_up(&sh->o_full[h], o_phase, &sh->gave_up, st);
             ok = __all_sync(0xffffffffu, ok);
@@ -515,9 +531,6 @@ __device__ void soften(const ChunkArgs& a, const BatchArgs& b, const Cursor& cur
                 }
             }
         }
-        __syncwarp();
-        have = more;
-        seg = next;
     }
 }
 

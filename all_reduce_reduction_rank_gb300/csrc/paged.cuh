@@ -210,6 +210,7 @@ struct Walk {
     Seq q;
     int loaded;
 
+    Walk() = default;   // in shared memory
     __device__ __forceinline__ explicit Walk(const Cursor& cur) : c(cur), q{0, 0, 0, 0}, loaded(-1) {}
 
     __device__ __forceinline__ bool next(const BatchArgs& b, int tm, Segment& seg, DevStatus* st)
