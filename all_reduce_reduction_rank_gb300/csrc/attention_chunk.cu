@@ -180,13 +180,13 @@ __device__ void issue(const ChunkArgs& a, const BatchArgs& b, const Cursor& cur,
     };
     // S of half h = its Q times the keys in `from`
     auto scores = [&](int h, int from) {
-        if (lane == 0 && ok) {
-            const uint32_t qa = smem_addr(q_tiles + h * kTileBytes<D>), ka = smem_addr(stages + from * kTileBytes<D>);
+        if (ok && elect_one()) {
+            const uint64_t qa = mma_operand(smem_addr(q_tiles + h * kTileBytes<D>), 1024, 16);
+            const uint64_t ka = mma_operand(smem_addr(stages + from * kTileBytes<D>), 1024, 16);
 #pragma unroll
             for (int k = 0; k < D / 16; ++k) {
-                const uint32_t off = (k / 4) * (kKeys * 128) + (k % 4) * 32;
-                mma_ss(tmem + h * kKeys, mma_operand(qa + off, 1024, 16), mma_operand(ka + off, 1024, 16), kScores,
-                       k > 0);
+                const uint32_t off = ((k / 4) * (kKeys * 128) + (k % 4) * 32) >> 4;
+                mma_ss(tmem + h * kKeys, qa + off, ka + off, kScores, k > 0);
             }
             mma_commit(&sh->s_full[h]);
         }
@@ -204,7 +204,7 @@ __device__ void issue(const ChunkArgs& a, const BatchArgs& b, const Cursor& cur,
                 tmem_after_sync();
                 scores(h, stage);
             }
-        if (lane == 0 && ok) mma_commit(&sh->empty[stage]);
+        if (ok && elect_one()) mma_commit(&sh->empty[stage]);
         __syncwarp();
         step(stage, phase);
         for (int i = 0; ok && i < tiles; ++i) {
@@ -236,12 +236,12 @@ __device__ void issue(const ChunkArgs& a, const BatchArgs& b, const Cursor& cur,
                 wait(&sh->p_full[h], p_phase[h]);
                 p_phase[h] ^= 1;
                 tmem_after_sync();
-                if (lane == 0 && ok) {
-                    const uint32_t va = smem_addr(stages + v_stage * kTileBytes<D>);
+                if (ok && elect_one()) {
+                    const uint64_t va = mma_operand(smem_addr(stages + v_stage * kTileBytes<D>), 1024, kKeys * 128);
 #pragma unroll
                     for (int k = 0; k < kKeys / 16; ++k)
-                        mma_ts(tmem + 2 * kKeys + h * D, tmem + h * kKeys + 8 * k,
-                               mma_operand(va + k * 2048, 1024, kKeys * 128), kValues, i > 0 || k > 0);
+                        mma_ts(tmem + 2 * kKeys + h * D, tmem + h * kKeys + 8 * k, va + k * (2048 >> 4), kValues,
+                               i > 0 || k > 0);
                     if (i + 1 == n[h]) mma_commit(&sh->o_full[h]);
                 }
                 __syncwarp();
@@ -253,7 +253,7 @@ __device__ void issue(const ChunkArgs& a, const BatchArgs& b, const Cursor& cur,
                     scores(h, k_stage);
                 }
             }
-            if (lane == 0 && ok) {
+            if (ok && elect_one()) {
                 mma_commit(&sh->empty[v_stage]);
                 if (more) mma_commit(&sh->empty[k_stage]);
             }
@@ -261,7 +261,7 @@ __device__ void issue(const ChunkArgs& a, const BatchArgs& b, const Cursor& cur,
         }
     }
     // nothing that was issued may still run when the tensor memory is freed
-    if (lane == 0) mma_commit(&sh->drained);
+    if (elect_one()) mma_commit(&sh->drained);
     __syncwarp();
     if (!wait_a_second(&sh->drained, 0, nullptr)) report_wait_timeout(st);
 }

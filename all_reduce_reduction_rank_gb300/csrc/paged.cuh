@@ -284,12 +284,17 @@ __device__ __forceinline__ void fence_proxy_async()
 // Bounded wait: false after about a second.
 __device__ __forceinline__ bool wait_a_second(uint64_t* bar, uint32_t parity, volatile int* stop)
 {
-    if (mbar_try_wait(bar, parity)) return true;
-    const uint64_t t0 = globaltimer_ns();
+    // the clock is read after 256 polls only: reading it costs as much as a tile's products
+    uint64_t t0 = 0;
     for (uint32_t i = 0; i < kMbarMaxPolls; ++i) {
         if (mbar_try_wait(bar, parity)) return true;
         if (stop && *stop) return false;
-        if ((i & 15) == 15 && globaltimer_ns() - t0 > 1000000000ull) return false;
+        if ((i & 255) == 255) {
+            if (t0 == 0)
+                t0 = globaltimer_ns();
+            else if (globaltimer_ns() - t0 > 1000000000ull)
+                return false;
+        }
     }
     return false;
 }
