@@ -50,10 +50,10 @@ struct ChunkShared {
     SplitShared split;
     uint32_t tmem;
     int gave_up, last[2];
-    // each softmax warp's place in the run: kept here, so that the loop over the
-    // keys has the registers
-    Walk<kKeys> walk[8];
-    Segment seg[8];
+    // each warp's place in the run: kept here, so that the loops over the keys
+    // have the registers
+    Walk<kKeys> walk[10];
+    Segment seg[10];
 };
 static_assert(sizeof(ChunkShared) <= 3072, "fits beside the tiles");
 
@@ -97,26 +97,51 @@ __device__ __forceinline__ void half_sync(int h)
         asm volatile("bar.sync 2, %0;" ::"n"(kHalf) : "memory");
 }
 
+// The warp's next segment, from and to shared memory.
+__device__ __forceinline__ bool next_segment(const BatchArgs& b, int tile_tokens, ChunkShared* sh, DevStatus* st)
+{
+    const int warp = threadIdx.x / 32;
+    Walk<kKeys> walk = sh->walk[warp];
+    Segment seg;
+    const bool more = walk.next(b, tile_tokens, seg, st);
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) {
+        sh->walk[warp] = walk;
+        sh->seg[warp] = seg;
+    }
+    __syncwarp();
+    return more;
+}
+
+// Waits with the whole warp; false for all its lanes, now and from then on,
+// once a wait of the CTA has run out.
+__device__ __forceinline__ void warp_wait(bool& ok, uint64_t* bar, uint32_t parity, ChunkShared* sh, DevStatus* st)
+{
+    if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return;
+    if (ok) ok = wait_or_give_up(bar, parity, &sh->gave_up, st);
+    ok = __all_sync(0xffffffffu, ok);
+}
+
 template <int D>
-__device__ void produce(const ChunkArgs& a, const BatchArgs& b, const Cursor& cur, uint8_t* stages, ChunkShared* sh,
+__device__ void produce(const ChunkArgs& a, const BatchArgs& b, uint8_t* stages, ChunkShared* sh,
                         DevStatus* st)
 {
     const int lane = threadIdx.x & 31;
     const int per_tile = kKeys / a.box_tokens;          // boxes of a tile along the keys: 2, 4 or 8
     const int box = lane % per_tile, panel = lane / per_tile;
     const bool mine = panel < D / 64;
-    Walk<kKeys> walk(cur);
-    Segment seg;
+    const Segment& seg = sh->seg[threadIdx.x / 32];
     int stage = 0;
     uint32_t phase = 0, issued = 0;
     bool ok = true;
-    while (ok && walk.next(b, 2 * a.half_tokens, seg, st)) {
+    while (ok && next_segment(b, 2 * a.half_tokens, sh, st)) {
         const int tiles = max(half_tile(a, seg, 0).tiles, half_tile(a, seg, 1).tiles);
         const int kv_head = seg.head % a.kv_heads, rank = seg.head / a.kv_heads;
         const int32_t* row = b.table + (size_t)seg.s * b.table_stride;
-        for (int j = seg.j0; ok && j < seg.j0 + tiles; ++j) {
+        const int j0 = seg.j0, key_lo = seg.span.key_lo, key_hi = seg.span.key_hi;
+        for (int j = j0; ok && j < j0 + tiles; ++j) {
             const int key = j * kKeys + box * a.box_tokens;
-            bool copy = mine && key < seg.span.key_hi && key + a.box_tokens > seg.span.key_lo;
+            bool copy = mine && key < key_hi && key + a.box_tokens > key_lo;
             int page = 0;
             if (copy) {
                 page = row[key >> b.page_shift];
@@ -127,9 +152,7 @@ __device__ void produce(const ChunkArgs& a, const BatchArgs& b, const Cursor& cu
             }
             const uint32_t bytes = __popc(__ballot_sync(0xffffffffu, copy)) * a.box_tokens * 128u;
             for (int v = 0; v < 2; ++v) {   // K, then V
-                if (issued >= (uint32_t)kStages<D>)
-                    ok = wait_or_give_up(&sh->empty[stage], phase ^ 1, &sh->gave_up, st);
-                ok = __all_sync(0xffffffffu, ok);
+                if (issued >= (uint32_t)kStages<D>) warp_wait(ok, &sh->empty[stage], phase ^ 1, sh, st);
                 if (!ok) break;
                 if (lane == 0) mbar_arrive_expect_tx(&sh->full[stage], bytes);
                 __syncwarp();
@@ -155,23 +178,19 @@ __device__ void produce(const ChunkArgs& a, const BatchArgs& b, const Cursor& cu
 }
 
 template <int DT, int D>
-__device__ void issue(const ChunkArgs& a, const BatchArgs& b, const Cursor& cur, uint8_t* q_tiles, uint8_t* stages,
-                      ChunkShared* sh, DevStatus* st)
+__device__ void issue(const ChunkArgs& a, const BatchArgs& b, uint8_t* q_tiles, uint8_t* stages, ChunkShared* sh,
+                      DevStatus* st)
 {
     constexpr uint32_t kScores = mma_shape(DT == AR_BF16, kKeys, false);
     constexpr uint32_t kValues = mma_shape(DT == AR_BF16, D, true);
     const int lane = threadIdx.x & 31;
     const uint32_t tmem = sh->tmem;
-    Walk<kKeys> walk(cur);
-    Segment seg;
+    const Segment& seg = sh->seg[threadIdx.x / 32];
     int stage = 0;                // of the next tile in the ring
     uint32_t phase = 0;
     uint32_t q_phase[2] = {0, 0}, p_phase[2] = {0, 0};
     bool ok = true;
-    auto wait = [&](uint64_t* bar, uint32_t parity) {
-        if (ok) ok = wait_or_give_up(bar, parity, &sh->gave_up, st);
-        ok = __all_sync(0xffffffffu, ok);
-    };
+    auto wait = [&](uint64_t* bar, uint32_t parity) { warp_wait(ok, bar, parity, sh, st); };
     auto step = [&](int& s, uint32_t& p) {
         if (++s == kStages<D>) {
             s = 0;
@@ -192,9 +211,9 @@ __device__ void issue(const ChunkArgs& a, const BatchArgs& b, const Cursor& cur,
         }
         __syncwarp();
     };
-    while (ok && walk.next(b, 2 * a.half_tokens, seg, st)) {
+    while (ok && next_segment(b, 2 * a.half_tokens, sh, st)) {
         const int n[2] = {half_tile(a, seg, 0).tiles, half_tile(a, seg, 1).tiles};
-        const int tiles = max(n[0], n[1]);
+        const int tiles = max(n[0], n[1]), j0 = seg.j0, key_lo = seg.span.key_lo, key_hi = seg.span.key_hi;
         if (tiles == 0) continue;
         wait(&sh->full[stage], phase);
         for (int h = 0; h < 2; ++h)
@@ -215,14 +234,16 @@ __device__ void issue(const ChunkArgs& a, const BatchArgs& b, const Cursor& cur,
             const uint32_t k_phase = phase;
             const bool more = i + 1 < tiles;
             if (more) step(stage, phase);
+            // both tiles are waited for while the tensor cores still have the last tile's products
             wait(&sh->full[v_stage], v_phase);
-            const int key0 = (seg.j0 + i) * kKeys;
-            if (key0 + kKeys > seg.span.key_hi || key0 < seg.span.key_lo) {
+            if (more) wait(&sh->full[k_stage], k_phase);
+            const int key0 = (j0 + i) * kKeys;
+            if (key0 + kKeys > key_hi || key0 < key_lo) {
                 // slots of these pages that no row sees may hold anything: their values count as 0
                 const uint32_t base = smem_addr(stages + v_stage * kTileBytes<D>);
                 for (int x = lane; x < kKeys * (D / 8); x += 32) {
                     const int r = x / (D / 8), c = x % (D / 8);
-                    if (key0 + r >= seg.span.key_hi || key0 + r < seg.span.key_lo) {
+                    if (key0 + r >= key_hi || key0 + r < key_lo) {
                         const uint32_t at = base + (c >> 3) * (kKeys * 128) + r * 128 + (c & 7) * 16;
                         asm volatile("st.shared.v4.b32 [%0], {%1,%1,%1,%1};" ::"r"(at), "r"(0) : "memory");
                     }
@@ -230,7 +251,6 @@ __device__ void issue(const ChunkArgs& a, const BatchArgs& b, const Cursor& cur,
                 fence_proxy_async();
                 __syncwarp();
             }
-            bool k_here = false;
             for (int h = 0; h < 2; ++h) {
                 if (i >= n[h]) continue;
                 wait(&sh->p_full[h], p_phase[h]);
@@ -245,13 +265,7 @@ __device__ void issue(const ChunkArgs& a, const BatchArgs& b, const Cursor& cur,
                     if (i + 1 == n[h]) mma_commit(&sh->o_full[h]);
                 }
                 __syncwarp();
-                if (i + 1 < n[h]) {
-                    if (!k_here) {
-                        wait(&sh->full[k_stage], k_phase);
-                        k_here = true;
-                    }
-                    scores(h, k_stage);
-                }
+                if (i + 1 < n[h]) scores(h, k_stage);
             }
             if (ok && elect_one()) {
                 mma_commit(&sh->empty[v_stage]);
@@ -290,8 +304,7 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b)
 }
 
 template <int DT, int D>
-__device__ void soften(const ChunkArgs& a, const BatchArgs& b, const Cursor& cur, uint8_t* q_tiles, ChunkShared* sh,
-                       DevStatus* st)
+__device__ void soften(const ChunkArgs& a, const BatchArgs& b, uint8_t* q_tiles, ChunkShared* sh, DevStatus* st)
 {
     using T = typename Payload<DT>::scalar_t;
     const int h = threadIdx.x / kHalf, row = threadIdx.x % kHalf, lane = threadIdx.x & 31;
@@ -333,23 +346,16 @@ __device__ void soften(const ChunkArgs& a, const BatchArgs& b, const Cursor& cur
 
     const int warp = threadIdx.x / 32;
     HalfTile x;
-    // the next segment, from and to shared memory
-    auto advance = [&](Walk<kKeys> walk) {
-        Segment seg;
-        const bool more = walk.next(b, 2 * a.half_tokens, seg, st);
-        __syncwarp();
-        if (lane == 0) {
-            sh->walk[warp] = walk;
-            sh->seg[warp] = seg;
-        }
-        __syncwarp();
+    auto advance = [&] {
+        const bool more = next_segment(b, 2 * a.half_tokens, sh, st);
         if (more) {
+            const Segment seg = sh->seg[warp];
             x = half_tile(a, seg, h);
             if (ok) load_q(seg, x);
         }
         return more;
     };
-    bool have = advance(Walk<kKeys>(cur));
+    bool have = advance();
     while (have) {
         // keys this row sees, and the range that every row of the half sees
         const int first = sh->seg[warp].q.c0 + x.tok0, j0 = sh->seg[warp].j0, tiles = x.tiles;
@@ -361,8 +367,7 @@ __device__ void soften(const ChunkArgs& a, const BatchArgs& b, const Cursor& cur
         uint64_t l2[2] = {0ull, 0ull};
         float l_before = 0.0f;   // the sum before the last move of m
         for (int i = 0; i < tiles; ++i) {
-            if (ok) ok = wait_or_give_up(&sh->s_full[h], s_phase, &sh->gave_up, st);
-            ok = __all_sync(0xffffffffu, ok);
+            warp_wait(ok, &sh->s_full[h], s_phase, sh, st);
             s_phase ^= 1;
             if (!ok) break;
             tmem_after_sync();
@@ -402,12 +407,12 @@ __device__ void soften(const ChunkArgs& a, const BatchArgs& b, const Cursor& cur
             const float ref = m == -INFINITY ? 0.0f : m;
             const uint64_t sc = pack2(a.scale_log2, a.scale_log2), off = pack2(-ref, -ref);
 #pragma unroll
-            for (int g = 0; g < 2; ++g) {
-                uint32_t pw[32];
+            for (int g = 0; g < 4; ++g) {
+                uint32_t pw[16];
 #pragma unroll
-                for (int k = 0; k < 32; ++k) {
+                for (int k = 0; k < 16; ++k) {
                     float y[2];
-                    const int e = 64 * g + 2 * k;
+                    const int e = 32 * g + 2 * k;
                     unpack2(fma2(pack2(s[e], s[e + 1]), sc, off), y[0], y[1]);
                     y[0] = ex2(y[0]);
                     y[1] = ex2(y[1]);
@@ -415,7 +420,7 @@ __device__ void soften(const ChunkArgs& a, const BatchArgs& b, const Cursor& cur
                     // rounded to the cache's type: the product's operand (at most half a step of it each)
                     pw[k] = Payload<DT>::narrow(y);
                 }
-                tmem_st32(s_at + 32 * g, pw);
+                tmem_st16(s_at + 16 * g, pw);
             }
             if (rescale && i > 0) {   // after the scores have left the registers
 #pragma unroll 1
@@ -435,7 +440,7 @@ __device__ void soften(const ChunkArgs& a, const BatchArgs& b, const Cursor& cur
         }
         const Segment seg = sh->seg[warp];
         const HalfTile done = x;
-        have = advance(sh->walk[warp]);
+        have = advance();
 
         // the row's sum and result
         float p, q, u, v;
@@ -443,8 +448,7 @@ __device__ void soften(const ChunkArgs& a, const BatchArgs& b, const Cursor& cur
         unpack2(l2[1], u, v);
         const float l = l_before + ((p + q) + (u + v));
         if (done.tiles > 0) {
-            if (ok) ok = wait_or_give_up(&sh->o_full[h], o_phase, &sh->gave_up, st);
-            ok = __all_sync(0xffffffffu, ok);
+            warp_wait(ok, &sh->o_full[h], o_phase, sh, st);
             o_phase ^= 1;
             tmem_after_sync();
         }
@@ -564,19 +568,20 @@ attention_chunk_kernel(const __grid_constant__ ChunkArgs a, const BatchArgs b, D
         pdl_release();
         return;
     }
+    if (warp < 10 && threadIdx.x % 32 == 0) sh->walk[warp] = Walk<kKeys>(cur);
     if (warp == 8) tmem_alloc(&sh->tmem, 512);
     tmem_before_sync();
     __syncthreads();
     tmem_after_sync();
     if (warp < 8) {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
-        soften<DT, D>(a, b, cur, q_tiles, sh, st);
+        soften<DT, D>(a, b, q_tiles, sh, st);
     } else {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
         if (warp == 8)
-            issue<DT, D>(a, b, cur, q_tiles, stages, sh, st);
+            issue<DT, D>(a, b, q_tiles, stages, sh, st);
         else if (warp == 9)
-            produce<D>(a, b, cur, stages, sh, st);
+            produce<D>(a, b, stages, sh, st);
     }
     pdl_release();
     tmem_before_sync();
