@@ -12,8 +12,9 @@
 //                   of the second product), statistics stay in registers
 //   warp 8          one thread issues S = Q K^T and O += P V
 //   warp 9          tensor copies of K and V tiles (pages) into a ring of stages
-//   warps 10, 11    none: with them the last four warps can hand registers to the
-//                   softmax warps, whose threads hold a row of 128 scores
+//   warps 10, 11    the next rows' queries of half 0, 1
+// The last four warps hand registers to the softmax warps, whose threads hold a
+// row of 128 scores.
 //
 // Tensor memory (512 columns): S/P of both halves, O of both halves.  Products
 // run in the order they are issued, and a half's S of tile j + 1 is issued
@@ -25,8 +26,8 @@
 // when a row's maximum passes it by more than 8, so O is rescaled a few times at
 // the start of a row and hardly ever later.
 //
-// Split of the keys over CTAs and the join of the parts: as in the decode
-// kernel (split_work), a half joining its own 128 rows.
+// Split of the keys over CTAs: as in the decode kernel (split_work); the parts,
+// up to 128 KB each, are joined by a second launch.
 #include "paged.cuh"
 #include "tmem.cuh"
 
@@ -40,31 +41,41 @@ constexpr int kTh = 384;
 constexpr int kSoftmaxRegs = 208, kOtherRegs = 88;
 constexpr float kSlack = 8.0f;
 
+using ChunkSplit = Split<kKeys, 2, 5>;
+
 template <int D> constexpr int kTileBytes = kKeys * D * 2;    // of K, of V, and of a half's Q
 template <int D> constexpr int kStages = D == 128 ? 5 : 10;
 template <int D> constexpr int kPartFloats = 2 * kHalf * (D + 2);
 
 struct ChunkShared {
     uint64_t full[10], empty[10];
-    uint64_t q_full[2], s_full[2], p_full[2], o_full[2], drained;
+    uint64_t q_full[2], q_empty[2], s_full[2], p_full[2], o_full[2], drained;
     SplitShared split;
     uint32_t tmem;
-    int gave_up, last[2];
+    int gave_up;
     // each warp's place in the run: kept here, so that the loops over the keys
     // have the registers
-    Walk<kKeys> walk[10];
-    Segment seg[10];
+    Walk<ChunkSplit> walk[12];
+    Segment seg[12];
 };
 static_assert(sizeof(ChunkShared) <= 3072, "fits beside the tiles");
 
 template <int D> constexpr int kSmem = (2 + kStages<D>) * kTileBytes<D> + 3072;
+
+// Rows whose keys were split: what the join needs, by the CTA of the first part.
+struct JoinWork {
+    unsigned parts;        // 0 or 1: nothing to join
+    int rank, kv_head;
+    int row0;              // packed row of the tile's first token
+    int rows[2];           // rows of its halves
+};
 
 struct ChunkArgs {
     const void* q[kMaxRanks];
     void* out[kMaxRanks];
     const CUtensorMap* maps;
     float* partial;
-    unsigned* arrived;
+    JoinWork* joins;
     size_t q_stride, out_stride;
     float scale_log2;
     int n, kv_heads, group;                  // query heads per kv head
@@ -89,19 +100,11 @@ __device__ __forceinline__ HalfTile half_tile(const ChunkArgs& a, const Segment&
     return x;
 }
 
-__device__ __forceinline__ void half_sync(int h)
-{
-    if (h == 0)
-        asm volatile("bar.sync 1, %0;" ::"n"(kHalf) : "memory");
-    else
-        asm volatile("bar.sync 2, %0;" ::"n"(kHalf) : "memory");
-}
-
 // The warp's next segment, from and to shared memory.
 __device__ __forceinline__ bool next_segment(const BatchArgs& b, int tile_tokens, ChunkShared* sh, DevStatus* st)
 {
     const int warp = threadIdx.x / 32;
-    Walk<kKeys> walk = sh->walk[warp];
+    Walk<ChunkSplit> walk = sh->walk[warp];
     Segment seg;
     const bool more = walk.next(b, tile_tokens, seg, st);
     __syncwarp();
@@ -177,6 +180,49 @@ __device__ void produce(const ChunkArgs& a, const BatchArgs& b, uint8_t* stages,
         }
 }
 
+// One warp a half: its queries, as soon as the last product that reads the
+// previous ones is done, so that they are there when the softmax warps come
+// from the rows before.
+template <int D>
+__device__ void load_queries(const ChunkArgs& a, const BatchArgs& b, int h, uint8_t* q_tile, ChunkShared* sh,
+                             DevStatus* st)
+{
+    const int lane = threadIdx.x & 31;
+    const Segment& seg = sh->seg[threadIdx.x / 32];
+    constexpr int C = D / 8;                   // 16-byte chunks of a row
+    const uint32_t base = smem_addr(q_tile);
+    uint32_t phase = 0;
+    bool first = true, ok = true;
+    while (ok && next_segment(b, 2 * a.half_tokens, sh, st)) {
+        const HalfTile x = half_tile(a, seg, h);
+        if (x.tiles == 0) continue;
+        if (!first) {
+            warp_wait(ok, &sh->q_empty[h], phase, sh, st);
+            phase ^= 1;
+            if (!ok) break;
+        }
+        first = false;
+        const int kv_head = seg.head % a.kv_heads, rank = seg.head / a.kv_heads;
+        const uint16_t* from = static_cast<const uint16_t*>(a.q[rank]) + (size_t)(seg.q.q0 + x.tok0) * a.q_stride +
+                               (size_t)kv_head * a.group * D + (lane % C) * 8;
+        int r = lane / C, tok = r / a.group, hd = r % a.group;
+        for (; r < kHalf; r += 32 / C) {
+            const bool there = r < x.rows;     // the others count as 0
+            const uint16_t* at = from + (there ? (size_t)tok * a.q_stride + (size_t)hd * D : 0);
+            const int c = lane % C;
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
+                             swizzled(base + (c >> 3) * (kHalf * 128), r, c & 7)),
+                         "l"(at), "r"(there ? 16 : 0)
+                         : "memory");
+            for (hd += 32 / C; hd >= a.group; hd -= a.group) ++tok;
+        }
+        asm volatile("cp.async.wait_all;" ::: "memory");
+        fence_proxy_async();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh->q_full[h]);
+    }
+}
+
 template <int DT, int D>
 __device__ void issue(const ChunkArgs& a, const BatchArgs& b, uint8_t* q_tiles, uint8_t* stages, ChunkShared* sh,
                       DevStatus* st)
@@ -198,7 +244,7 @@ __device__ void issue(const ChunkArgs& a, const BatchArgs& b, uint8_t* q_tiles, 
         }
     };
     // S of half h = its Q times the keys in `from`
-    auto scores = [&](int h, int from) {
+    auto scores = [&](int h, int from, bool last) {
         if (ok && elect_one()) {
             const uint64_t qa = mma_operand(smem_addr(q_tiles + h * kTileBytes<D>), 1024, 16);
             const uint64_t ka = mma_operand(smem_addr(stages + from * kTileBytes<D>), 1024, 16);
@@ -208,6 +254,7 @@ __device__ void issue(const ChunkArgs& a, const BatchArgs& b, uint8_t* q_tiles, 
                 mma_ss(tmem + h * kKeys, qa + off, ka + off, kScores, k > 0);
             }
             mma_commit(&sh->s_full[h]);
+            if (last) mma_commit(&sh->q_empty[h]);
         }
         __syncwarp();
     };
@@ -221,7 +268,7 @@ __device__ void issue(const ChunkArgs& a, const BatchArgs& b, uint8_t* q_tiles, 
                 wait(&sh->q_full[h], q_phase[h]);
                 q_phase[h] ^= 1;
                 tmem_after_sync();
-                scores(h, stage);
+                scores(h, stage, n[h] == 1);
             }
         if (ok && elect_one()) mma_commit(&sh->empty[stage]);
         __syncwarp();
@@ -265,7 +312,7 @@ __device__ void issue(const ChunkArgs& a, const BatchArgs& b, uint8_t* q_tiles, 
                     if (i + 1 == n[h]) mma_commit(&sh->o_full[h]);
                 }
                 __syncwarp();
-                if (i + 1 < n[h]) scores(h, k_stage);
+                if (i + 1 < n[h]) scores(h, k_stage, i + 2 == n[h]);
             }
             if (ok && elect_one()) {
                 mma_commit(&sh->empty[v_stage]);
@@ -303,56 +350,45 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b)
     return d;
 }
 
+// Lane i of four consecutive ones holds pieces w[0..3] of row i; after: piece i
+// of rows 0..3.
+__device__ __forceinline__ void transpose4(uint32_t (&w)[4][4], int lane)
+{
+#pragma unroll
+    for (int d = 1; d < 4; d <<= 1) {
+        const bool up = lane & d;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if (i & d) continue;
+            // swap w[i + d] of the lane without the bit for w[i] of the lane with it
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const uint32_t give = up ? w[i][k] : w[i + d][k];
+                const uint32_t got = __shfl_xor_sync(0xffffffffu, give, d);
+                if (up)
+                    w[i][k] = got;
+                else
+                    w[i + d][k] = got;
+            }
+        }
+    }
+}
+
 template <int DT, int D>
-__device__ void soften(const ChunkArgs& a, const BatchArgs& b, uint8_t* q_tiles, ChunkShared* sh, DevStatus* st)
+__device__ void soften(const ChunkArgs& a, const BatchArgs& b, ChunkShared* sh, DevStatus* st)
 {
     using T = typename Payload<DT>::scalar_t;
     const int h = threadIdx.x / kHalf, row = threadIdx.x % kHalf, lane = threadIdx.x & 31;
     const uint32_t lanes = (uint32_t)(row & ~31) << 16;
     const uint32_t s_at = sh->tmem + lanes + h * kKeys, o_at = sh->tmem + lanes + 2 * kKeys + h * D;
-    uint8_t* q_tile = q_tiles + h * kTileBytes<D>;
     bool ok = true;
     uint32_t s_phase = 0, o_phase = 0;
-
-    auto load_q = [&](const Segment& seg, const HalfTile& x) {
-        // 16 threads (8 for D = 64) a row, a row after the other, swizzled as the copies swizzle K
-        if (x.tiles == 0) return;
-        int group = a.group;
-        asm volatile("" : "+r"(group));   // the rows' places are computed here, not kept in registers over the loop
-        const int kv_head = seg.head % a.kv_heads, rank = seg.head / a.kv_heads;
-        const T* from = static_cast<const T*>(a.q[rank]) + (size_t)kv_head * a.group * D;
-        constexpr int C = D / 8;
-        uint4 v[C];
-#pragma unroll
-        for (int k = 0; k < C; ++k) {
-            const int i = k * kHalf + row, r = i / C, c = i % C;
-            v[k] = make_uint4(0u, 0u, 0u, 0u);
-            if (r < x.rows)
-                v[k] = ld16(from + (size_t)(seg.q.q0 + x.tok0 + r / group) * a.q_stride + (size_t)(r % group) * D +
-                            8 * c);
-        }
-#pragma unroll
-        for (int k = 0; k < C; ++k) {
-            const int i = k * kHalf + row, r = i / C, c = i % C;
-            const uint32_t at = swizzled(smem_addr(q_tile) + (c >> 3) * (kHalf * 128), r, c & 7);
-            asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(at), "r"(v[k].x), "r"(v[k].y), "r"(v[k].z),
-                         "r"(v[k].w)
-                         : "memory");
-        }
-        fence_proxy_async();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sh->q_full[h]);
-    };
 
     const int warp = threadIdx.x / 32;
     HalfTile x;
     auto advance = [&] {
         const bool more = next_segment(b, 2 * a.half_tokens, sh, st);
-        if (more) {
-            const Segment seg = sh->seg[warp];
-            x = half_tile(a, seg, h);
-            if (ok) load_q(seg, x);
-        }
+        if (more) x = half_tile(a, sh->seg[warp], h);
         return more;
     };
     bool have = advance();
@@ -453,23 +489,27 @@ __device__ void soften(const ChunkArgs& a, const BatchArgs& b, uint8_t* q_tiles,
             tmem_after_sync();
         }
         const int kv_head = seg.head % a.kv_heads, rank = seg.head / a.kv_heads;
-        T* to = static_cast<T*>(a.out[rank]) + (size_t)(seg.q.q0 + done.tok0 + row / a.group) * a.out_stride +
-                (size_t)(kv_head * a.group + row % a.group) * D;
+        // 32 columns of the warp's rows: four lanes swap their 16-byte pieces, so that a store
+        // writes 64 bytes of 8 rows, not 16 of 32
+        T* to[4];
+        bool there[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const int r = (row & ~3) + k;
+            there[k] = r < done.rows && ok;
+            to[k] = static_cast<T*>(a.out[rank]) + (size_t)(seg.q.q0 + done.tok0 + r / a.group) * a.out_stride +
+                    (size_t)(kv_head * a.group + r % a.group) * D + 8 * (row & 3);
+        }
         auto store32 = [&](const float* o, int k) {
+            uint32_t w[4][4];
 #pragma unroll
-            for (int e = 0; e < 32; e += 8) {
-                float w[8];
+            for (int e = 0; e < 16; ++e) w[e / 4][e % 4] = Payload<DT>::narrow(o + 2 * e);
+            transpose4(w, lane);
 #pragma unroll
-                for (int y = 0; y < 8; ++y) w[y] = o[e + y];
-                uint4 r;
-                r.x = Payload<DT>::narrow(w);
-                r.y = Payload<DT>::narrow(w + 2);
-                r.z = Payload<DT>::narrow(w + 4);
-                r.w = Payload<DT>::narrow(w + 6);
-                st16_next(to + k + e, r);
-            }
+            for (int e = 0; e < 4; ++e)
+                if (there[e]) st16_next(to[e] + k, make_uint4(w[e][0], w[e][1], w[e][2], w[e][3]));
         };
-        if (seg.whole) {
+        if (seg.parts == 1) {
             const float inv = l == 0.0f ? 0.0f : 1.0f / l;
 #pragma unroll
             for (int k = 0; k < D; k += 32) {
@@ -480,7 +520,7 @@ __device__ void soften(const ChunkArgs& a, const BatchArgs& b, uint8_t* q_tiles,
                 }
 #pragma unroll
                 for (int e = 0; e < 32; ++e) o[e] = done.tiles > 0 ? o[e] * inv : 0.0f;
-                if (row < done.rows && ok) store32(o, k);
+                store32(o, k);
             }
         } else {
             // column after column, so that the warp's rows are consecutive words
@@ -496,42 +536,16 @@ __device__ void soften(const ChunkArgs& a, const BatchArgs& b, uint8_t* q_tiles,
                 }
             __stcg(part + D * kHalf + row, m);
             __stcg(part + (D + 1) * kHalf + row, l);
-            __threadfence();
-            half_sync(h);
-            if (row == 0) {
-                unsigned* count = &a.arrived[2 * seg.first_cta + h];
-                sh->last[h] = atomicAdd(count, 1u) + 1 == seg.parts;
-                if (sh->last[h]) *count = 0;   // for the next call
-            }
-            half_sync(h);
-            if (sh->last[h]) {
-                __threadfence();
-                auto part_of = [&](unsigned k) {
-                    return a.partial + (size_t)part_slot(seg.first_cta, k) * kPartFloats<D> + h * (kHalf * (D + 2));
-                };
-                float top = -INFINITY, sum = 0.0f;
-                for (unsigned k = 0; k < seg.parts; ++k) top = fmaxf(top, __ldcg(part_of(k) + D * kHalf + row));
-                for (unsigned k = 0; k < seg.parts; ++k) {
-                    const float pm = __ldcg(part_of(k) + D * kHalf + row);
-                    if (pm != -INFINITY) sum = fmaf(__ldcg(part_of(k) + (D + 1) * kHalf + row), ex2(pm - top), sum);
-                }
-                const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-#pragma unroll 1
-                for (int k = 0; k < D; k += 32) {
-                    float o[32];
-#pragma unroll
-                    for (int e = 0; e < 32; ++e) o[e] = 0.0f;
-                    for (unsigned y = 0; y < seg.parts; ++y) {
-                        const float* from = part_of(y);
-                        const float pm = __ldcg(from + D * kHalf + row);
-                        if (pm == -INFINITY) continue;   // a part that saw nothing wrote no columns
-                        const float w = ex2(pm - top);
-#pragma unroll
-                        for (int e = 0; e < 32; ++e) o[e] = fmaf(__ldcg(from + (k + e) * kHalf + row), w, o[e]);
+            if (seg.slot & 1) {   // the first part
+                if (row == 0) {
+                    JoinWork& j = a.joins[blockIdx.x];
+                    if (h == 0) {
+                        j.rank = rank;
+                        j.kv_head = kv_head;
+                        j.row0 = seg.q.q0 + done.tok0;
+                        j.parts = seg.parts;
                     }
-#pragma unroll
-                    for (int e = 0; e < 32; ++e) o[e] *= inv;
-                    if (row < done.rows) store32(o, k);
+                    j.rows[h] = done.rows;
                 }
             }
         }
@@ -553,7 +567,8 @@ attention_chunk_kernel(const __grid_constant__ ChunkArgs a, const BatchArgs b, D
             mbar_init(&sh->empty[i], 1);
         }
         for (int h = 0; h < 2; ++h) {
-            mbar_init(&sh->q_full[h], kHalf / 32);
+            mbar_init(&sh->q_full[h], 1);
+            mbar_init(&sh->q_empty[h], 1);
             mbar_init(&sh->s_full[h], 1);
             mbar_init(&sh->p_full[h], kHalf / 32);
             mbar_init(&sh->o_full[h], 1);
@@ -563,25 +578,28 @@ attention_chunk_kernel(const __grid_constant__ ChunkArgs a, const BatchArgs b, D
         sh->gave_up = 0;
     }
     pdl_acquire();
-    const Cursor cur = split_work<kKeys, kTh>(b, 2 * a.half_tokens, a.n * a.kv_heads, a.min_units, &sh->split, st);
-    if (cur.g >= cur.end) {
+    if (threadIdx.x == 0) a.joins[blockIdx.x].parts = 0;
+    Cursor cur;
+    if (!split_work<ChunkSplit, kTh>(b, 2 * a.half_tokens, a.n * a.kv_heads, a.min_units, &sh->split, cur, st)) {
         pdl_release();
         return;
     }
-    if (warp < 10 && threadIdx.x % 32 == 0) sh->walk[warp] = Walk<kKeys>(cur);
+    if (threadIdx.x % 32 == 0) sh->walk[warp] = Walk<ChunkSplit>(cur);
     if (warp == 8) tmem_alloc(&sh->tmem, 512);
     tmem_before_sync();
     __syncthreads();
     tmem_after_sync();
     if (warp < 8) {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
-        soften<DT, D>(a, b, q_tiles, sh, st);
+        soften<DT, D>(a, b, sh, st);
     } else {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
         if (warp == 8)
             issue<DT, D>(a, b, q_tiles, stages, sh, st);
         else if (warp == 9)
             produce<D>(a, b, stages, sh, st);
+        else
+            load_queries<D>(a, b, warp - 10, q_tiles + (warp - 10) * kTileBytes<D>, sh, st);
     }
     pdl_release();
     tmem_before_sync();
@@ -592,6 +610,53 @@ attention_chunk_kernel(const __grid_constant__ ChunkArgs a, const BatchArgs b, D
     }
 }
 
+// Joins the parts of the rows whose keys were split, in the order of the keys:
+// o = sum 2^(m_k - m) o_k / sum 2^(m_k - m) l_k.  A launch of its own, so that
+// every SM takes a share of what one CTA of the first launch would read alone;
+// a block takes 16 columns of a half's 128 rows.
+constexpr int kJoinColumns = 16;
+
+template <int DT, int D>
+__global__ void __launch_bounds__(kHalf)
+attention_join_kernel(const __grid_constant__ ChunkArgs a)
+{
+    using T = typename Payload<DT>::scalar_t;
+    pdl_acquire();
+    pdl_release();
+    const unsigned f = blockIdx.x;
+    const int h = blockIdx.y / (D / kJoinColumns), d = blockIdx.y % (D / kJoinColumns) * kJoinColumns;
+    const JoinWork j = a.joins[f];
+    const int row = threadIdx.x;
+    if (j.parts < 2 || row >= j.rows[h]) return;
+    auto part_of = [&](unsigned k) {
+        return a.partial + (size_t)part_slot(f, k) * kPartFloats<D> + h * (kHalf * (D + 2)) + row;
+    };
+    float top = -INFINITY;
+#pragma unroll 8
+    for (unsigned k = 0; k < j.parts; ++k) top = fmaxf(top, __ldcg(part_of(k) + D * kHalf));
+    float o[kJoinColumns], sum = 0.0f;
+#pragma unroll
+    for (int e = 0; e < kJoinColumns; ++e) o[e] = 0.0f;
+#pragma unroll 4
+    for (unsigned k = 0; k < j.parts; ++k) {
+        const float* from = part_of(k);
+        const float m = __ldcg(from + D * kHalf);
+        if (m == -INFINITY) continue;   // a part that saw nothing wrote no columns
+        const float w = ex2(m - top);
+        sum = fmaf(__ldcg(from + (D + 1) * kHalf), w, sum);
+#pragma unroll
+        for (int e = 0; e < kJoinColumns; ++e) o[e] = fmaf(__ldcg(from + (d + e) * kHalf), w, o[e]);
+    }
+    const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+    const int r = row + h * a.half_tokens * a.group;   // rows of half 0 come first
+    T* to = static_cast<T*>(a.out[j.rank]) + (size_t)(j.row0 + r / a.group) * a.out_stride +
+            (size_t)(j.kv_head * a.group + r % a.group) * D + d;
+#pragma unroll
+    for (int e = 0; e < kJoinColumns; ++e) o[e] *= inv;
+#pragma unroll
+    for (int e = 0; e < kJoinColumns; e += 8) st16_next(to + e, round_vec<DT>(o + e));
+}
+
 }  // namespace
 
 size_t attention_chunk_partial_floats(const Handle& h, int head_dim)
@@ -599,7 +664,7 @@ size_t attention_chunk_partial_floats(const Handle& h, int head_dim)
     return (size_t)(2 * h.sm_count) * (size_t)(2 * kHalf * (head_dim + 2));
 }
 
-size_t attention_chunk_counters(const Handle& h) { return (size_t)(2 * h.sm_count); }
+size_t attention_chunk_join_bytes(const Handle& h) { return (size_t)h.sm_count * sizeof(JoinWork); }
 
 int launch_attention_chunk(KvCache& kv, const ar_batch_t& b, const AttnCall& c, int window, cudaStream_t s)
 {
@@ -611,7 +676,7 @@ int launch_attention_chunk(KvCache& kv, const ar_batch_t& b, const AttnCall& c, 
     }
     a.maps = kv.maps;
     a.partial = kv.partial;
-    a.arrived = kv.arrived;
+    a.joins = static_cast<JoinWork*>(kv.joins);
     a.q_stride = c.q_stride;
     a.out_stride = c.out_stride;
     a.scale_log2 = c.scale * 1.4426950408889634f;
@@ -633,8 +698,10 @@ int launch_attention_chunk(KvCache& kv, const ar_batch_t& b, const AttnCall& c, 
         rec_begin(h, s);
         const cudaError_t e = launch_kernel(h, attention_chunk_kernel<DT, D>, dim3((unsigned)h.sm_count), dim3(kTh),
                                             kSmem<D>, s, a, batch_args(kv, b, window), h.status);
-        rec_end(h, s, AR_K_ATTENTION_CHUNK, moved);
-        return e == cudaSuccess ? launch_status() : AR_ERR_CUDA;
+        const cudaError_t e2 = launch_kernel(h, attention_join_kernel<DT, D>,
+                                             dim3((unsigned)h.sm_count, 2 * D / kJoinColumns), dim3(kHalf), 0, s, a);
+        rec_end(h, s, AR_K_ATTENTION_CHUNK, moved, 2);
+        return e == cudaSuccess && e2 == cudaSuccess ? launch_status() : AR_ERR_CUDA;
     };
     using BF = std::integral_constant<int, AR_BF16>;
     using HF = std::integral_constant<int, AR_F16>;

@@ -33,6 +33,8 @@ constexpr int kRows = 16;
 constexpr int kCtas = 2;                     // per SM
 constexpr float kSlack = 8.0f;               // log2 of how far p may pass 1
 
+using DecodeSplit = Split<kKeys, 0, 0>;
+
 template <int D> constexpr int kTileBytes = kKeys * D * 2;
 template <int D> constexpr int kStages = D == 128 ? 3 : 6;
 template <int D> constexpr int kPartFloats = kRows * (D + 2);
@@ -123,7 +125,7 @@ __device__ void produce(const DecodeArgs& a, const BatchArgs& b, const Cursor& c
     // lane -> one copy of the tile
     const int box = lane % per_page, panel = (lane / per_page) % panels, is_v = lane / (per_page * panels);
     const bool mine = is_v < 2;
-    Walk<kKeys> walk(cur);
+    Walk<DecodeSplit> walk(cur);
     Segment seg;
     int stage = 0;
     uint32_t phase = 0;
@@ -179,7 +181,7 @@ __device__ void consume(const DecodeArgs& a, const BatchArgs& b, const Cursor& c
     constexpr int NT = D / 8;       // 8-wide column tiles of the output
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int r0 = lane >> 2, col = (lane & 3) * 2;
-    Walk<kKeys> walk(cur);
+    Walk<DecodeSplit> walk(cur);
     Segment seg;
     int stage = 0;
     uint32_t phase = 0;
@@ -369,7 +371,7 @@ __device__ void consume(const DecodeArgs& a, const BatchArgs& b, const Cursor& c
             for (int w = 0; w < kWarps; ++w) top = fmaxf(top, sh->m[w][r]);
             for (int w = 0; w < kWarps; ++w)
                 sum += sh->m[w][r] == -INFINITY ? 0.0f : sh->l[w][r] * ex2(sh->m[w][r] - top);
-            if (seg.whole) {
+            if (seg.parts == 1) {
                 const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
                 store_row4(r, d, make_float4(z.x * inv, z.y * inv, z.z * inv, z.w * inv));
             } else {
@@ -380,7 +382,7 @@ __device__ void consume(const DecodeArgs& a, const BatchArgs& b, const Cursor& c
                 }
             }
         }
-        if (!seg.whole) {
+        if (seg.parts > 1) {
             __threadfence();
             consumers_sync();
             if (tid == 0) {
@@ -435,9 +437,8 @@ attention_decode_kernel(const __grid_constant__ DecodeArgs a, const BatchArgs b,
         sh->gave_up = 0;
     }
     pdl_acquire();
-    const Cursor cur =
-        split_work<kKeys, kTh>(b, a.tm, a.n * a.kv_heads * a.head_groups, a.min_units, &sh->split, st);
-    if (cur.g >= cur.end) {
+    Cursor cur;
+    if (!split_work<DecodeSplit, kTh>(b, a.tm, a.n * a.kv_heads * a.head_groups, a.min_units, &sh->split, cur, st)) {
         pdl_release();
         return;
     }

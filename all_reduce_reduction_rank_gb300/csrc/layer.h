@@ -21,7 +21,8 @@ struct KvCache {
     void* v[kMaxRanks] = {};
     CUtensorMap* maps = nullptr;     // device: n maps of K, then n of V
     float* partial = nullptr;        // device: partial results of rows split over CTAs
-    unsigned* arrived = nullptr;     // device: partials arrived, by the CTA in which the rows' first key tile lies
+    unsigned* arrived = nullptr;     // device: decode kernel's partials arrived, by the CTA of the first part
+    void* joins = nullptr;           // device: the chunk kernel's rows to join, by the CTA of the first part
 };
 
 // A call's batch and cache geometry, passed by value to the kernels.
@@ -75,7 +76,7 @@ int launch_rope_append(KvCache& kv, const ar_batch_t& b, const RopeCall& c, cuda
 size_t attention_decode_partial_floats(const Handle& h, int head_dim);
 size_t attention_decode_counters(const Handle& h);
 size_t attention_chunk_partial_floats(const Handle& h, int head_dim);
-size_t attention_chunk_counters(const Handle& h);
+size_t attention_chunk_join_bytes(const Handle& h);
 int launch_attention_decode(KvCache& kv, const ar_batch_t& b, const AttnCall& c, int window, cudaStream_t s);
 int launch_attention_chunk(KvCache& kv, const ar_batch_t& b, const AttnCall& c, int window, cudaStream_t s);
 

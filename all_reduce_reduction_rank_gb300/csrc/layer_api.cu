@@ -210,10 +210,11 @@ int ar_kv_create(ar_handle hd, const ar_kv_desc_t* d, void* const* k, void* cons
                 return AR_ERR_INVALID;
         const size_t floats = std::max(attention_decode_partial_floats(*h, d->head_dim),
                                        attention_chunk_partial_floats(*h, d->head_dim));
-        const size_t counters = std::max(attention_decode_counters(*h), attention_chunk_counters(*h));
+        const size_t counters = attention_decode_counters(*h), join_bytes = attention_chunk_join_bytes(*h);
         const size_t map_bytes = 2u * (size_t)h->n * sizeof(CUtensorMap);
         if (cudaMalloc(&kv.maps, map_bytes) != cudaSuccess || cudaMalloc(&kv.partial, floats * 4u) != cudaSuccess ||
             cudaMalloc(&kv.arrived, counters * sizeof(unsigned)) != cudaSuccess ||
+            cudaMalloc(&kv.joins, join_bytes) != cudaSuccess ||
             cudaMemcpy(kv.maps, maps, map_bytes, cudaMemcpyHostToDevice) != cudaSuccess ||
             cudaMemset(kv.arrived, 0, counters * sizeof(unsigned)) != cudaSuccess ||
             cudaDeviceSynchronize() != cudaSuccess) {
@@ -221,6 +222,7 @@ int ar_kv_create(ar_handle hd, const ar_kv_desc_t* d, void* const* k, void* cons
             if (kv.maps) cudaFree(kv.maps);
             if (kv.partial) cudaFree(kv.partial);
             if (kv.arrived) cudaFree(kv.arrived);
+            if (kv.joins) cudaFree(kv.joins);
             return AR_ERR_CUDA;
         }
         return AR_OK;
@@ -268,6 +270,7 @@ int ar_kv_destroy(ar_kv k)
         if (cudaFree(kv->maps) != cudaSuccess) r = AR_ERR_CUDA;
         if (cudaFree(kv->partial) != cudaSuccess) r = AR_ERR_CUDA;
         if (cudaFree(kv->arrived) != cudaSuccess) r = AR_ERR_CUDA;
+        if (cudaFree(kv->joins) != cudaSuccess) r = AR_ERR_CUDA;
         return r;
     });
     k->magic = 0;
@@ -316,6 +319,7 @@ int ar_paged_attention(ar_kv k, const ar_batch_t* b, const void* const* q, void*
     if (rc != AR_OK) return rc;
     const uint64_t moved = 2ull * h.n * b->tokens * row;
     note(h, AR_OP_PAGED_ATTENTION, b->tokens * row, moved, moved, (cudaStream_t)stream);
+    if (b->tokens && !few) h.last.launches = 2;
     return AR_OK;
 }
 

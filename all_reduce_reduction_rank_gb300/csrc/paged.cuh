@@ -37,18 +37,25 @@ __device__ __forceinline__ Seq load_seq(const BatchArgs& b, int s, DevStatus* st
 }
 
 // ---- split of the work ------------------------------------------------------------
-// The unit is one tile of KT keys against one row tile: TM consecutive new
-// tokens of a sequence, with the query heads of one head group.  A (sequence,
-// row tile) pair counts its tiles between the first key any of its rows sees
-// and the last; at least one, so that rows that see nothing are written too.
-// The units of all (head group, sequence, row tile) triples, in that order,
-// are cut into equal runs, one per CTA, whatever the lengths are: every CTA
-// gets the same number of key tiles, and only the first and the last triple
-// of its run can be shared with other CTAs.
+// A row tile is TM consecutive new tokens of a sequence with the query heads of
+// one head group; it costs one unit per tile of KT keys between the first key
+// any of its rows sees and the last (at least one, so that rows that see
+// nothing are written too), and W units for its start and end.  The units of
+// all (head group, sequence, row tile) triples, in that order, are cut into
+// equal runs, one per CTA, whatever the lengths are.  A cut that falls within
+// SNAP units of a triple's edge moves to that edge: the triples that stay cut
+// are joined afterwards, which costs more than that imbalance.  Only the first
+// and the last triple of a run can be shared with other CTAs.
+
+template <int KT_, int W_, int SNAP_>
+struct Split {
+    static constexpr int KT = KT_, W = W_, SNAP = SNAP_;
+    static_assert(SNAP >= W, "a cut that stays lies among the key tiles");
+};
 
 struct Span {
     int key_lo, key_hi;   // keys that some row of the tile sees (key_hi <= key_lo: none)
-    int j_lo, units;      // first key tile, number of tiles (>= 1)
+    int j_lo, tiles;      // first key tile, number of tiles (>= 1)
 };
 
 template <int KT>
@@ -60,45 +67,46 @@ __device__ __forceinline__ Span span_of(const Seq& q, int tm, int t, int window)
     p.key_hi = max(last, 0);
     p.key_lo = window > 0 ? max(first - window + 1, 0) : 0;
     p.j_lo = p.key_lo / KT;
-    p.units = max((p.key_hi + KT - 1) / KT - p.j_lo, 1);
+    p.tiles = max((p.key_hi + KT - 1) / KT - p.j_lo, 1);
     return p;
 }
 
+typedef unsigned long long u64;
+
 struct Cursor {
-    unsigned long long g, end;   // next unit and one past the last of this CTA's run
-    unsigned long long per_head; // units of one head group
-    unsigned long long total;    // units of the call
+    u64 begin;                   // first unit of the current triple
+    u64 end;                     // where the next CTA's run begins, before it is moved to an edge
+    u64 total;                   // units of the call
     unsigned ctas;               // CTAs that share them
-    int head, s, t, off;         // the triple that unit g is in, and its place in it
+    int head, s, t;              // the current triple
+    int tile;                    // its first key tile of this CTA
 };
 
-__device__ __forceinline__ unsigned long long run_begin(unsigned long long total, unsigned ctas, unsigned c)
-{
-    return total * c / ctas;
-}
+__device__ __forceinline__ u64 run_begin(u64 total, unsigned ctas, unsigned c) { return total * c / ctas; }
 
-// The CTA whose run holds unit u.
-__device__ __forceinline__ unsigned cta_of(unsigned long long total, unsigned ctas, unsigned long long u)
+// The last CTA whose run begins at or before unit u.
+__device__ __forceinline__ unsigned cta_of(u64 total, unsigned ctas, u64 u)
 {
     return (unsigned)(((u + 1) * ctas - 1) / total);
 }
 
 struct SplitShared {
-    unsigned long long warp_sum[32];
-    unsigned long long total;
-    unsigned long long off;
+    u64 warp_sum[32];
+    u64 off;
     int s;
 };
 
-// Called by all NT threads.  `min_units`: a run is at least that long (the
-// last ones may be empty), so that small calls do not pay for joins.
-template <int KT, int NT>
-__device__ Cursor split_work(const BatchArgs& b, int tm, int heads, int min_units, SplitShared* sh, DevStatus* st)
+// Called by all NT threads; false for a CTA with nothing to do.  `min_units`:
+// a run is at least that long, so that small calls do not pay for joins.
+template <typename S, int NT>
+__device__ bool split_work(const BatchArgs& b, int tm, int heads, int min_units, SplitShared* sh, Cursor& c,
+                           DevStatus* st)
 {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int per = (b.seqs + NT - 1) / NT;
     const int s0 = min(tid * per, b.seqs), s1 = min(s0 + per, b.seqs);
-    unsigned long long mine = 0;
+    auto units_of = [&](const Seq& q, int t) { return (unsigned)(span_of<S::KT>(q, tm, t, b.window).tiles + S::W); };
+    u64 mine = 0;
     // long sequences' row tiles are counted by the whole warp
     for (int k = 0; k < per; ++k) {
         const int s = s0 + k;
@@ -107,7 +115,7 @@ __device__ Cursor split_work(const BatchArgs& b, int tm, int heads, int min_unit
         const int nt = (q.nq + tm - 1) / tm;
         const bool is_long = nt > 8;
         if (!is_long)
-            for (int t = 0; t < nt; ++t) mine += (unsigned)span_of<KT>(q, tm, t, b.window).units;
+            for (int t = 0; t < nt; ++t) mine += units_of(q, t);
         unsigned todo = __ballot_sync(0xffffffffu, is_long);
         while (todo) {
             const int src = __ffs(todo) - 1;
@@ -118,48 +126,45 @@ __device__ Cursor split_work(const BatchArgs& b, int tm, int heads, int min_unit
             w.len = __shfl_sync(0xffffffffu, q.len, src);
             w.c0 = w.len - w.nq;
             const int wt = (w.nq + tm - 1) / tm;
-            unsigned long long sum = 0;
-            for (int t = lane; t < wt; t += 32) sum += (unsigned)span_of<KT>(w, tm, t, b.window).units;
+            u64 sum = 0;
+            for (int t = lane; t < wt; t += 32) sum += units_of(w, t);
             for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
             if (lane == src) mine += sum;
         }
     }
-    unsigned long long incl = mine;
+    u64 incl = mine;
     for (int o = 1; o < 32; o <<= 1) {
-        const unsigned long long x = __shfl_up_sync(0xffffffffu, incl, o);
+        const u64 x = __shfl_up_sync(0xffffffffu, incl, o);
         if (lane >= o) incl += x;
     }
     if (lane == 31) sh->warp_sum[warp] = incl;
     __syncthreads();
-    unsigned long long before = 0, all = 0;
+    u64 before = 0, per_head = 0;
 #pragma unroll
     for (int w = 0; w < NT / 32; ++w) {
         if (w < warp) before += sh->warp_sum[w];
-        all += sh->warp_sum[w];
+        per_head += sh->warp_sum[w];
     }
-    Cursor c;
-    c.per_head = all;
-    c.total = all * (unsigned)heads;
+    c.total = per_head * (unsigned)heads;
     c.ctas = gridDim.x;
-    const unsigned long long most = (c.total + min_units - 1) / min_units;
+    const u64 most = (c.total + min_units - 1) / min_units;
     if (most < c.ctas) c.ctas = (unsigned)most;
-    c.g = c.end = 0;
-    c.head = c.s = c.t = c.off = 0;
-    if (blockIdx.x >= c.ctas) return c;   // the whole CTA
-    c.g = run_begin(c.total, c.ctas, blockIdx.x);
+    if (blockIdx.x >= c.ctas) return false;   // the whole CTA
+    const u64 g = run_begin(c.total, c.ctas, blockIdx.x);
     c.end = run_begin(c.total, c.ctas, blockIdx.x + 1);
-    c.head = (int)(c.g / c.per_head);
-    const unsigned long long in_head = c.g - c.head * c.per_head;
-    const unsigned long long excl = before + incl - mine;
+    c.head = (int)(g / per_head);
+    const u64 in_head = g - c.head * per_head;
+    const u64 excl = before + incl - mine;
     if (in_head >= excl && in_head < excl + mine) {
         // this thread's sequences hold it
-        unsigned long long at = excl;
+        u64 at = excl;
         for (int s = s0; s < s1; ++s) {
-            const Seq q = load_seq(b, s, st);
-            const int nt = (q.nq + tm - 1) / tm;
-            unsigned long long sum = 0;
-            if (s + 1 < s1)
-                for (int t = 0; t < nt; ++t) sum += (unsigned)span_of<KT>(q, tm, t, b.window).units;
+            u64 sum = 0;
+            if (s + 1 < s1) {
+                const Seq q = load_seq(b, s, st);
+                const int nt = (q.nq + tm - 1) / tm;
+                for (int t = 0; t < nt; ++t) sum += units_of(q, t);
+            }
             if (s + 1 == s1 || in_head < at + sum) {
                 sh->s = s;
                 sh->off = in_head - at;
@@ -171,26 +176,32 @@ __device__ Cursor split_work(const BatchArgs& b, int tm, int heads, int min_unit
     __syncthreads();
     c.s = sh->s;
     // the row tile inside the sequence: every warp walks it, 32 tiles at a time
-    unsigned long long off = sh->off;
+    u64 off = sh->off;
     const Seq q = load_seq(b, c.s, st);
     const int nt = (q.nq + tm - 1) / tm;
-    for (int t0 = 0; t0 < nt; t0 += 32) {
+    c.t = 0;
+    for (int t0 = 0; nt > 1; t0 += 32) {
         const int t = t0 + lane;
-        unsigned long long u = t < nt ? (unsigned)span_of<KT>(q, tm, t, b.window).units : 0, in = u;
+        const u64 u = t < nt ? units_of(q, t) : 0;
+        u64 in = u;
         for (int o = 1; o < 32; o <<= 1) {
-            const unsigned long long x = __shfl_up_sync(0xffffffffu, in, o);
+            const u64 x = __shfl_up_sync(0xffffffffu, in, o);
             if (lane >= o) in += x;
         }
         const unsigned here = __ballot_sync(0xffffffffu, in > off);
         if (here) {
             const int src = __ffs(here) - 1;
             c.t = t0 + src;
-            c.off = (int)(off - __shfl_sync(0xffffffffu, in - u, src));
+            off -= __shfl_sync(0xffffffffu, in - u, src);
             break;
         }
+        if (t0 + 32 >= nt) break;   // not reached: the tiles' units cover `off`
         off -= __shfl_sync(0xffffffffu, in, 31);
     }
-    return c;
+    c.begin = g - off;
+    const int units = (int)units_of(q, c.t), o = (int)off, snap = min(S::SNAP, units / 2);
+    c.tile = o <= snap ? 0 : units - o <= snap ? units - S::W : o - S::W;
+    return true;
 }
 
 // One triple's part in this CTA's run.
@@ -199,12 +210,11 @@ struct Segment {
     Span span;
     int head, s, t;
     int j0, j1;                       // key tiles of this CTA
-    bool whole;                       // the triple lies in this run entirely
-    unsigned first_cta, parts, slot;  // if not whole: where it begins, its parts, this CTA's partial slot
+    unsigned first_cta, parts, slot;  // CTA of its first part, its parts (1: whole), this CTA's partial slot
 };
 
 // Walks a run.  Every warp keeps its own copy; all read the same values.
-template <int KT>
+template <typename S>
 struct Walk {
     Cursor c;
     Seq q;
@@ -215,48 +225,55 @@ struct Walk {
 
     __device__ __forceinline__ bool next(const BatchArgs& b, int tm, Segment& seg, DevStatus* st)
     {
-        if (c.g >= c.end) return false;
         for (;;) {
+            if (c.begin >= c.end) return false;
             if (loaded != c.s) {
                 q = load_seq(b, c.s, st);
                 loaded = c.s;
             }
-            if (c.t * tm < q.nq) break;
-            c.t = 0;
-            if (++c.s == b.seqs) {
-                c.s = 0;
-                ++c.head;
+            if (c.t * tm >= q.nq) {
+                c.t = 0;
+                if (++c.s == b.seqs) {
+                    c.s = 0;
+                    ++c.head;
+                }
+                continue;
             }
-        }
-        seg.q = q;
-        seg.span = span_of<KT>(q, tm, c.t, b.window);
-        seg.head = c.head;
-        seg.s = c.s;
-        seg.t = c.t;
-        const unsigned long long left = c.end - c.g;
-        const int rest = seg.span.units - c.off;
-        const int take = left < (unsigned long long)rest ? (int)left : rest;
-        seg.j0 = seg.span.j_lo + c.off;
-        seg.j1 = seg.j0 + take;
-        seg.whole = take == seg.span.units;
-        if (!seg.whole) {
-            const unsigned long long begin = c.g - c.off;
-            seg.first_cta = cta_of(c.total, c.ctas, begin);
-            seg.parts = cta_of(c.total, c.ctas, begin + seg.span.units - 1) - seg.first_cta + 1;
-            seg.slot = 2 * blockIdx.x + (seg.first_cta == blockIdx.x ? 1 : 0);
-        }
-        c.g += take;
-        if (take == rest) {
+            seg.span = span_of<S::KT>(q, tm, c.t, b.window);
+            const int units = seg.span.tiles + S::W, snap = min(S::SNAP, units / 2);
+            const u64 left = c.end - c.begin;
+            int stop = seg.span.tiles;   // one past this CTA's last tile
+            bool last = false;
+            if (left < (u64)units) {
+                const int o = (int)left;
+                last = true;
+                if (o <= snap) return false;
+                if (units - o > snap) stop = o - S::W;
+            }
+            const int start = c.tile;
+            seg.first_cta = 0;
+            seg.parts = 1;
+            seg.slot = 0;
+            if (start > 0 || stop < seg.span.tiles) {
+                seg.first_cta = cta_of(c.total, c.ctas, c.begin + snap);
+                seg.parts = cta_of(c.total, c.ctas, c.begin + units - snap - 1) - seg.first_cta + 1;
+                seg.slot = 2 * blockIdx.x + (seg.first_cta == blockIdx.x ? 1 : 0);
+            }
+            seg.q = q;
+            seg.head = c.head;
+            seg.s = c.s;
+            seg.t = c.t;
+            seg.j0 = seg.span.j_lo + start;
+            seg.j1 = seg.span.j_lo + stop;
+            c.begin = last ? c.end : c.begin + units;
+            c.tile = 0;
             ++c.t;
-            c.off = 0;
-        } else {
-            c.off += take;
+            if (start < stop) return true;   // else the run's first cut moved to the end of this triple
         }
-        return true;
     }
 };
 
-// Partial slot of part i of a triple that begins in CTA f.
+// Partial slot of part i of a triple whose first part is CTA f's.
 __device__ __forceinline__ unsigned part_slot(unsigned f, unsigned i) { return i == 0 ? 2 * f + 1 : 2 * (f + i); }
 
 // ---- copies, waits, arithmetic -------------------------------------------------------
