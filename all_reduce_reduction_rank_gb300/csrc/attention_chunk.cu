@@ -203,18 +203,27 @@ __device__ void load_queries(const ChunkArgs& a, const BatchArgs& b, int h, uint
         }
         first = false;
         const int kv_head = seg.head % a.kv_heads, rank = seg.head / a.kv_heads;
-        const uint16_t* from = static_cast<const uint16_t*>(a.q[rank]) + (size_t)(seg.q.q0 + x.tok0) * a.q_stride +
-                               (size_t)kv_head * a.group * D + (lane % C) * 8;
-        int r = lane / C, tok = r / a.group, hd = r % a.group;
-        for (; r < kHalf; r += 32 / C) {
+        // lanes 0 .. C - 1 take the chunks of one row, the next C of the next; a row's place moves on
+        // by additions alone
+        constexpr int R = 32 / C;              // rows a step
+        const int c = lane % C;
+        const size_t wrap = a.q_stride - (size_t)a.group * D;   // from past a token's last head to the next's first
+        const uint16_t* at = static_cast<const uint16_t*>(a.q[rank]) + (size_t)(seg.q.q0 + x.tok0) * a.q_stride +
+                             (size_t)kv_head * a.group * D + 8 * c;
+        int r = lane / C, hd = r;
+        at += (size_t)r * D;
+        for (; hd >= a.group; hd -= a.group) at += wrap;
+        uint32_t to = base + (c >> 3) * (kHalf * 128) + r * 128;
+#pragma unroll 8
+        for (int k = 0; k < kHalf / R; ++k) {
             const bool there = r < x.rows;     // the others count as 0
-            const uint16_t* at = from + (there ? (size_t)tok * a.q_stride + (size_t)hd * D : 0);
-            const int c = lane % C;
-            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
-                             swizzled(base + (c >> 3) * (kHalf * 128), r, c & 7)),
-                         "l"(at), "r"(there ? 16 : 0)
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to + (((c ^ r) & 7) << 4)),
+                         "l"(there ? (const void*)at : a.q[rank]), "r"(there ? 16 : 0)
                          : "memory");
-            for (hd += 32 / C; hd >= a.group; hd -= a.group) ++tok;
+            r += R;
+            to += R * 128;
+            at += R * D;
+            for (hd += R; hd >= a.group; hd -= a.group) at += wrap;
         }
         asm volatile("cp.async.wait_all;" ::: "memory");
         fence_proxy_async();
@@ -511,7 +520,7 @@ __device__ void soften(const ChunkArgs& a, const BatchArgs& b, ChunkShared* sh, 
         };
         if (seg.parts == 1) {
             const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-#pragma unroll
+#pragma unroll 1
             for (int k = 0; k < D; k += 32) {
                 float o[32];
                 if (done.tiles > 0 && ok) {
@@ -526,7 +535,7 @@ __device__ void soften(const ChunkArgs& a, const BatchArgs& b, ChunkShared* sh, 
             // column after column, so that the warp's rows are consecutive words
             float* part = a.partial + (size_t)seg.slot * kPartFloats<D> + h * (kHalf * (D + 2));
             if (done.tiles > 0 && ok)
-#pragma unroll
+#pragma unroll 1
                 for (int k = 0; k < D; k += 32) {
                     float o[32];
                     tmem_ld32(o, o_at + k);
@@ -577,6 +586,8 @@ attention_chunk_kernel(const __grid_constant__ ChunkArgs a, const BatchArgs b, D
         mbar_init_fence();
         sh->gave_up = 0;
     }
+    // written by the host when the caches were registered: no need to wait for the launch before
+    if (threadIdx.x < 2 * a.n) prefetch_map(a.maps + threadIdx.x);
     pdl_acquire();
     if (threadIdx.x == 0) a.joins[blockIdx.x].parts = 0;
     Cursor cur;

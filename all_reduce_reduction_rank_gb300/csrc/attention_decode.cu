@@ -436,6 +436,8 @@ attention_decode_kernel(const __grid_constant__ DecodeArgs a, const BatchArgs b,
         mbar_init_fence();
         sh->gave_up = 0;
     }
+    // written by the host when the caches were registered: no need to wait for the launch before
+    if (threadIdx.x < 2 * a.n) prefetch_map(a.maps + threadIdx.x);
     pdl_acquire();
     Cursor cur;
     if (!split_work<DecodeSplit, kTh>(b, a.tm, a.n * a.kv_heads * a.head_groups, a.min_units, &sh->split, cur, st)) {

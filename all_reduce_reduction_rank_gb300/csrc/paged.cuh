@@ -43,8 +43,9 @@ __device__ __forceinline__ Seq load_seq(const BatchArgs& b, int s, DevStatus* st
 // nothing are written too), and W units for its start and end.  The units of
 // all (head group, sequence, row tile) triples, in that order, are cut into
 // equal runs, one per CTA, whatever the lengths are.  A cut that falls within
-// SNAP units of a triple's edge moves to that edge: the triples that stay cut
-// are joined afterwards, which costs more than that imbalance.  Only the first
+// an eighth of a run (W to SNAP units) of a triple's edge moves to that edge: the
+// triples that stay cut are joined afterwards, which costs more than that
+// imbalance.  Only the first
 // and the last triple of a run can be shared with other CTAs.
 
 template <int KT_, int W_, int SNAP_>
@@ -78,16 +79,23 @@ struct Cursor {
     u64 end;                     // where the next CTA's run begins, before it is moved to an edge
     u64 total;                   // units of the call
     unsigned ctas;               // CTAs that share them
+    int snap;                    // an eighth of a run, W to SNAP
     int head, s, t;              // the current triple
     int tile;                    // its first key tile of this CTA
 };
 
-__device__ __forceinline__ u64 run_begin(u64 total, unsigned ctas, unsigned c) { return total * c / ctas; }
+// a / b; most calls are small enough for the 32-bit division, a fraction of the other's time
+__device__ __forceinline__ u64 quotient(u64 a, u64 b)
+{
+    return ((a | b) >> 32) == 0 ? (u64)((unsigned)a / (unsigned)b) : a / b;
+}
+
+__device__ __forceinline__ u64 run_begin(u64 total, unsigned ctas, unsigned c) { return quotient(total * c, ctas); }
 
 // The last CTA whose run begins at or before unit u.
 __device__ __forceinline__ unsigned cta_of(u64 total, unsigned ctas, u64 u)
 {
-    return (unsigned)(((u + 1) * ctas - 1) / total);
+    return (unsigned)quotient((u + 1) * ctas - 1, total);
 }
 
 struct SplitShared {
@@ -102,9 +110,11 @@ template <typename S, int NT>
 __device__ bool split_work(const BatchArgs& b, int tm, int heads, int min_units, SplitShared* sh, Cursor& c,
                            DevStatus* st)
 {
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int per = (b.seqs + NT - 1) / NT;
-    const int s0 = min(tid * per, b.seqs), s1 = min(s0 + per, b.seqs);
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    // consecutive sequences for a warp's lanes; few sequences are spread over the warps
+    const int of_warp = (b.seqs + NT / 32 - 1) / (NT / 32), per = (of_warp + 31) / 32;
+    const int w0 = min(warp * of_warp, b.seqs), w1 = min(w0 + of_warp, b.seqs);
+    const int s0 = min(w0 + lane * per, w1), s1 = min(s0 + per, w1);
     auto units_of = [&](const Seq& q, int t) { return (unsigned)(span_of<S::KT>(q, tm, t, b.window).tiles + S::W); };
     u64 mine = 0;
     // long sequences' row tiles are counted by the whole warp
@@ -152,10 +162,12 @@ __device__ bool split_work(const BatchArgs& b, int tm, int heads, int min_units,
     if (blockIdx.x >= c.ctas) return false;   // the whole CTA
     const u64 g = run_begin(c.total, c.ctas, blockIdx.x);
     c.end = run_begin(c.total, c.ctas, blockIdx.x + 1);
-    c.head = (int)(g / per_head);
+    const u64 eighth = quotient(c.total, c.ctas) / 8;
+    c.snap = eighth < (u64)S::W ? S::W : eighth > (u64)S::SNAP ? S::SNAP : (int)eighth;
+    c.head = (int)quotient(g, per_head);
     const u64 in_head = g - c.head * per_head;
     const u64 excl = before + incl - mine;
-    if (in_head >= excl && in_head < excl + mine) {
+    if (in_head >= excl && in_head < excl + mine) {   // (false without sequences: mine is 0)
         // this thread's sequences hold it
         u64 at = excl;
         for (int s = s0; s < s1; ++s) {
@@ -199,7 +211,7 @@ __device__ bool split_work(const BatchArgs& b, int tm, int heads, int min_units,
         off -= __shfl_sync(0xffffffffu, in, 31);
     }
     c.begin = g - off;
-    const int units = (int)units_of(q, c.t), o = (int)off, snap = min(S::SNAP, units / 2);
+    const int units = (int)units_of(q, c.t), o = (int)off, snap = min(c.snap, units / 2);
     c.tile = o <= snap ? 0 : units - o <= snap ? units - S::W : o - S::W;
     return true;
 }
@@ -240,7 +252,7 @@ struct Walk {
                 continue;
             }
             seg.span = span_of<S::KT>(q, tm, c.t, b.window);
-            const int units = seg.span.tiles + S::W, snap = min(S::SNAP, units / 2);
+            const int units = seg.span.tiles + S::W, snap = min(c.snap, units / 2);
             const u64 left = c.end - c.begin;
             int stop = seg.span.tiles;   // one past this CTA's last tile
             bool last = false;
@@ -286,6 +298,11 @@ __device__ __forceinline__ void page_copy(void* smem_dst, const CUtensorMap* map
                  "[%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(smem_addr(smem_dst)),
                  "l"(map), "r"(d), "r"(slot), "r"(head), "r"(page), "r"(smem_addr(bar))
                  : "memory");
+}
+
+__device__ __forceinline__ void prefetch_map(const CUtensorMap* map)
+{
+    asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
 }
 
 __device__ __forceinline__ void mbar_arrive(uint64_t* bar)
