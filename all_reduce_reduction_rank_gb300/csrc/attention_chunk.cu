@@ -10,9 +10,10 @@
 //   warps 0-3, 4-7  softmax of half 0, 1: thread = row.  Scores come from tensor
 //                   memory, probabilities go back over them (16 bits, A operand
 //                   of the second product), statistics stay in registers
-//   warp 8          one thread issues S = Q K^T and O += P V
+//   warp 8          one thread issues S = Q K^T and O += P V of both halves in turn
+//                   (a warp a half let them drift into step: 1364 for 1530 TFLOP/s)
 //   warp 9          tensor copies of K and V tiles (pages) into a ring of stages
-//   warps 10, 11    the next rows' queries of half 0, 1
+//   warp 10         tensor copies of the next rows' queries
 // The last four warps hand registers to the softmax warps, whose threads hold a
 // row of 128 scores.
 //
@@ -49,7 +50,7 @@ template <int D> constexpr int kPartFloats = 2 * kHalf * (D + 2);
 
 struct ChunkShared {
     uint64_t full[10], empty[10];
-    uint64_t q_full[2], q_empty[2], s_full[2], p_full[2], o_full[2], drained;
+    uint64_t q_full[2], q_empty[2], s_full[2], p_full[2][2], o_full[2], drained;
     SplitShared split;
     uint32_t tmem;
     int gave_up;
@@ -71,12 +72,12 @@ struct JoinWork {
 };
 
 struct ChunkArgs {
-    const void* q[kMaxRanks];
+    CUtensorMap q[kMaxRanks];                // boxes of a half's tokens and of a kv head's query heads
     void* out[kMaxRanks];
     const CUtensorMap* maps;
     float* partial;
     JoinWork* joins;
-    size_t q_stride, out_stride;
+    size_t out_stride;
     float scale_log2;
     int n, kv_heads, group;                  // query heads per kv head
     int half_tokens;                         // new tokens of a half: 128 / group
@@ -180,56 +181,42 @@ __device__ void produce(const ChunkArgs& a, const BatchArgs& b, uint8_t* stages,
         }
 }
 
-// One warp a half: its queries, as soon as the last product that reads the
-// previous ones is done, so that they are there when the softmax warps come
-// from the rows before.
+// The halves' queries, as soon as the last product that reads the previous
+// ones is done, so that they are there when the softmax warps come from the rows
+// before.  A box may reach into the next sequence's tokens or past the last:
+// those rows are computed and not written.
 template <int D>
-__device__ void load_queries(const ChunkArgs& a, const BatchArgs& b, int h, uint8_t* q_tile, ChunkShared* sh,
-                             DevStatus* st)
+__device__ void load_queries(const ChunkArgs& a, const BatchArgs& b, uint8_t* q_tiles, ChunkShared* sh, DevStatus* st)
 {
     const int lane = threadIdx.x & 31;
     const Segment& seg = sh->seg[threadIdx.x / 32];
-    constexpr int C = D / 8;                   // 16-byte chunks of a row
-    const uint32_t base = smem_addr(q_tile);
-    uint32_t phase = 0;
-    bool first = true, ok = true;
+    uint32_t phase[2] = {0, 0};
+    bool first[2] = {true, true}, ok = true, in_flight[2] = {false, false};
     while (ok && next_segment(b, 2 * a.half_tokens, sh, st)) {
-        const HalfTile x = half_tile(a, seg, h);
-        if (x.tiles == 0) continue;
-        if (!first) {
-            warp_wait(ok, &sh->q_empty[h], phase, sh, st);
-            phase ^= 1;
-            if (!ok) break;
-        }
-        first = false;
         const int kv_head = seg.head % a.kv_heads, rank = seg.head / a.kv_heads;
-        // lanes 0 .. C - 1 take the chunks of one row, the next C of the next; a row's place moves on
-        // by additions alone
-        constexpr int R = 32 / C;              // rows a step
-        const int c = lane % C;
-        const size_t wrap = a.q_stride - (size_t)a.group * D;   // from past a token's last head to the next's first
-        const uint16_t* at = static_cast<const uint16_t*>(a.q[rank]) + (size_t)(seg.q.q0 + x.tok0) * a.q_stride +
-                             (size_t)kv_head * a.group * D + 8 * c;
-        int r = lane / C, hd = r;
-        at += (size_t)r * D;
-        for (; hd >= a.group; hd -= a.group) at += wrap;
-        uint32_t to = base + (c >> 3) * (kHalf * 128) + r * 128;
-#pragma unroll 8
-        for (int k = 0; k < kHalf / R; ++k) {
-            const bool there = r < x.rows;     // the others count as 0
-            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to + (((c ^ r) & 7) << 4)),
-                         "l"(there ? (const void*)at : a.q[rank]), "r"(there ? 16 : 0)
-                         : "memory");
-            r += R;
-            to += R * 128;
-            at += R * D;
-            for (hd += R; hd >= a.group; hd -= a.group) at += wrap;
+        for (int h = 0; ok && h < 2; ++h) {
+            const HalfTile x = half_tile(a, seg, h);
+            if (x.tiles == 0) continue;
+            if (!first[h]) {
+                warp_wait(ok, &sh->q_empty[h], phase[h], sh, st);
+                phase[h] ^= 1;
+                if (!ok) break;
+            }
+            first[h] = false;
+            in_flight[h] = true;
+            if (lane == 0) {
+                mbar_arrive_expect_tx(&sh->q_full[h], (uint32_t)(a.half_tokens * a.group * D * 2));
+                for (int d = 0; d < D; d += 64)
+                    box_copy(q_tiles + h * kTileBytes<D> + (d / 64) * (kHalf * 128), &a.q[rank], d, kv_head * a.group,
+                             seg.q.q0 + x.tok0, &sh->q_full[h]);
+            }
+            __syncwarp();
         }
-        asm volatile("cp.async.wait_all;" ::: "memory");
-        fence_proxy_async();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sh->q_full[h]);
     }
+    // after a wait that ran out: the last copies, whose phase is the one after the last q_empty
+    if (!ok)
+        for (int h = 0; h < 2; ++h)
+            if (in_flight[h]) wait_a_second(&sh->q_full[h], phase[h], nullptr);
 }
 
 template <int DT, int D>
@@ -309,18 +296,23 @@ __device__ void issue(const ChunkArgs& a, const BatchArgs& b, uint8_t* q_tiles, 
             }
             for (int h = 0; h < 2; ++h) {
                 if (i >= n[h]) continue;
-                wait(&sh->p_full[h], p_phase[h]);
-                p_phase[h] ^= 1;
-                tmem_after_sync();
-                if (ok && elect_one()) {
-                    const uint64_t va = mma_operand(smem_addr(stages + v_stage * kTileBytes<D>), 1024, kKeys * 128);
+                // the probabilities come in two parts: the product over the first 64 keys runs while
+                // the softmax warps do the others
 #pragma unroll
-                    for (int k = 0; k < kKeys / 16; ++k)
-                        mma_ts(tmem + 2 * kKeys + h * D, tmem + h * kKeys + 8 * k, va + k * (2048 >> 4), kValues,
-                               i > 0 || k > 0);
-                    if (i + 1 == n[h]) mma_commit(&sh->o_full[h]);
+                for (int part = 0; part < 2; ++part) {
+                    wait(&sh->p_full[h][part], p_phase[h]);
+                    tmem_after_sync();
+                    if (ok && elect_one()) {
+                        const uint64_t va = mma_operand(smem_addr(stages + v_stage * kTileBytes<D>), 1024, kKeys * 128);
+#pragma unroll
+                        for (int k = 4 * part; k < 4 * part + 4; ++k)
+                            mma_ts(tmem + 2 * kKeys + h * D, tmem + h * kKeys + 8 * k, va + k * (2048 >> 4), kValues,
+                                   i > 0 || k > 0);
+                        if (part == 1 && i + 1 == n[h]) mma_commit(&sh->o_full[h]);
+                    }
+                    __syncwarp();
                 }
-                __syncwarp();
+                p_phase[h] ^= 1;
                 if (i + 1 < n[h]) scores(h, k_stage, i + 2 == n[h]);
             }
             if (ok && elect_one()) {
@@ -356,6 +348,13 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b)
 {
     uint64_t d;
     asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+
+__device__ __forceinline__ float max3(float a, float b, float c)
+{
+    float d;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
     return d;
 }
 
@@ -429,12 +428,11 @@ __device__ void soften(const ChunkArgs& a, const BatchArgs& b, ChunkShared* sh, 
             }
             float mx[4] = {s[0], s[1], s[2], s[3]};
 #pragma unroll
-            for (int k = 4; k < kKeys; k += 4) {
-                mx[0] = fmaxf(mx[0], s[k]);
-                mx[1] = fmaxf(mx[1], s[k + 1]);
-                mx[2] = fmaxf(mx[2], s[k + 2]);
-                mx[3] = fmaxf(mx[3], s[k + 3]);
-            }
+            for (int k = 4; k + 8 <= kKeys; k += 8)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) mx[e] = max3(mx[e], s[k + e], s[k + 4 + e]);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) mx[e] = fmaxf(mx[e], s[kKeys - 4 + e]);
             const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * a.scale_log2;
             const bool move = top > m + kSlack;
             const bool rescale = __any_sync(0xffffffffu, move);
@@ -448,6 +446,17 @@ __device__ void soften(const ChunkArgs& a, const BatchArgs& b, ChunkShared* sh, 
                 unpack2(l2[1], u, v);
                 l_before = (l_before + ((p + q) + (u + v))) * f;
                 l2[0] = l2[1] = 0ull;
+            }
+            if (rescale && i > 0) {
+#pragma unroll 1
+                for (int k = 0; k < D; k += 16) {
+                    float o[16];
+                    tmem_ld16(o, o_at + k);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) o[e] *= f;
+                    tmem_st16(o_at + k, reinterpret_cast<const uint32_t*>(o));
+                }
             }
             const float ref = m == -INFINITY ? 0.0f : m;
             const uint64_t sc = pack2(a.scale_log2, a.scale_log2), off = pack2(-ref, -ref);
@@ -466,22 +475,13 @@ __device__ void soften(const ChunkArgs& a, const BatchArgs& b, ChunkShared* sh, 
                     pw[k] = Payload<DT>::narrow(y);
                 }
                 tmem_st16(s_at + 16 * g, pw);
-            }
-            if (rescale && i > 0) {   // after the scores have left the registers
-#pragma unroll 1
-                for (int k = 0; k < D; k += 32) {
-                    float o[32];
-                    tmem_ld32(o, o_at + k);
-                    tmem_wait_ld();
-#pragma unroll
-                    for (int e = 0; e < 32; ++e) o[e] *= f;
-                    tmem_st32(o_at + k, reinterpret_cast<const uint32_t*>(o));
+                if (g & 1) {
+                    tmem_wait_st();
+                    tmem_before_sync();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&sh->p_full[h][g / 2]);
                 }
             }
-            tmem_wait_st();
-            tmem_before_sync();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&sh->p_full[h]);
         }
         const Segment seg = sh->seg[warp];
         const HalfTile done = x;
@@ -579,7 +579,8 @@ attention_chunk_kernel(const __grid_constant__ ChunkArgs a, const BatchArgs b, D
             mbar_init(&sh->q_full[h], 1);
             mbar_init(&sh->q_empty[h], 1);
             mbar_init(&sh->s_full[h], 1);
-            mbar_init(&sh->p_full[h], kHalf / 32);
+            mbar_init(&sh->p_full[h][0], kHalf / 32);
+            mbar_init(&sh->p_full[h][1], kHalf / 32);
             mbar_init(&sh->o_full[h], 1);
         }
         mbar_init(&sh->drained, 1);
@@ -609,8 +610,8 @@ attention_chunk_kernel(const __grid_constant__ ChunkArgs a, const BatchArgs b, D
             issue<DT, D>(a, b, q_tiles, stages, sh, st);
         else if (warp == 9)
             produce<D>(a, b, stages, sh, st);
-        else
-            load_queries<D>(a, b, warp - 10, q_tiles + (warp - 10) * kTileBytes<D>, sh, st);
+        else if (warp == 10)
+            load_queries<D>(a, b, q_tiles, sh, st);
     }
     pdl_release();
     tmem_before_sync();
@@ -681,19 +682,22 @@ int launch_attention_chunk(KvCache& kv, const ar_batch_t& b, const AttnCall& c, 
 {
     Handle& h = *kv.h;
     ChunkArgs a{};
+    const int group = c.q_heads / kv.d.kv_heads;
     for (int r = 0; r < h.n; ++r) {
-        a.q[r] = c.q[r];
+        const size_t dims[3] = {(size_t)kv.d.head_dim, (size_t)c.q_heads, b.tokens};
+        const size_t strides[2] = {(size_t)kv.d.head_dim * 2, c.q_stride * 2};
+        const unsigned box[3] = {64, (unsigned)group, (unsigned)(kHalf / group)};
+        if (int rc = encode_map(kv, &a.q[r], 3, c.q[r], dims, strides, box)) return rc;
         a.out[r] = c.out[r];
     }
     a.maps = kv.maps;
     a.partial = kv.partial;
     a.joins = static_cast<JoinWork*>(kv.joins);
-    a.q_stride = c.q_stride;
     a.out_stride = c.out_stride;
     a.scale_log2 = c.scale * 1.4426950408889634f;
     a.n = h.n;
     a.kv_heads = kv.d.kv_heads;
-    a.group = c.q_heads / kv.d.kv_heads;
+    a.group = group;
     a.half_tokens = kHalf / a.group;
     a.box_tokens = kv.box_tokens;
     a.min_units = 4;

@@ -17,6 +17,7 @@ struct KvCache {
     Handle* h = nullptr;
     ar_kv_desc_t d{};
     int box_tokens = 0;              // tokens of one tensor copy: min(page_size, 64)
+    void* encode = nullptr;          // the driver's cuTensorMapEncodeTiled
     void* k[kMaxRanks] = {};
     void* v[kMaxRanks] = {};
     CUtensorMap* maps = nullptr;     // device: n maps of K, then n of V
@@ -53,6 +54,11 @@ struct AttnCall {
     size_t q_stride, out_stride;     // elements
     float scale;
 };
+
+// A tensor map over 16-bit elements of the cache's type with the 128-byte
+// swizzle; strides in bytes, of the second dimension on.
+int encode_map(const KvCache& kv, CUtensorMap* map, int dims, const void* base, const size_t* size,
+               const size_t* strides, const unsigned* box);
 
 Handle* handle_of(ar_handle h);      // nullptr if it is not a handle
 

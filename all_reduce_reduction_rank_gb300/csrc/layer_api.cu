@@ -145,19 +145,25 @@ int check_attention(int n, const ar_kv_desc_t& d, const ar_batch_t* b, const Att
     return AR_OK;
 }
 
-CUresult encode(PFN_cuTensorMapEncodeTiled_v12000 fn, CUtensorMap* m, const ar_kv_desc_t& d, int box_tokens, void* base)
-{
-    const cuuint64_t dims[4] = {(cuuint64_t)d.head_dim, (cuuint64_t)d.page_size, (cuuint64_t)d.kv_heads,
-                                (cuuint64_t)d.pages};
-    const cuuint64_t strides[3] = {d.token_stride * 2, d.head_stride * 2, d.page_stride * 2};
-    const cuuint32_t box[4] = {64, (cuuint32_t)box_tokens, 1, 1};
-    const cuuint32_t ones[4] = {1, 1, 1, 1};
-    return fn(m, d.dtype == AR_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4, base, dims,
-              strides, box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-}
-
 }  // namespace
+
+int argb::encode_map(const KvCache& kv, CUtensorMap* map, int dims, const void* base, const size_t* size,
+                     const size_t* strides, const unsigned* box)
+{
+    cuuint64_t sz[5], st[5];
+    cuuint32_t bx[5], ones[5];
+    for (int i = 0; i < dims; ++i) {
+        sz[i] = size[i];
+        if (i > 0) st[i - 1] = strides[i - 1];
+        bx[i] = box[i];
+        ones[i] = 1;
+    }
+    const auto type = kv.d.dtype == AR_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+    const CUresult rc = ((PFN_cuTensorMapEncodeTiled_v12000)kv.encode)(
+        map, type, (cuuint32_t)dims, const_cast<void*>(base), sz, st, bx, ones, CU_TENSOR_MAP_INTERLEAVE_NONE,
+        CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return rc == CUDA_SUCCESS ? AR_OK : AR_ERR_INVALID;
+}
 
 struct ar_kv_ctx {
     uint32_t magic;
@@ -203,10 +209,14 @@ int ar_kv_create(ar_handle hd, const ar_kv_desc_t* d, void* const* k, void* cons
                 cudaSuccess ||
             found != cudaDriverEntryPointSuccess || !fn)
             return AR_ERR_CUDA;
+        kv.encode = fn;
         alignas(64) CUtensorMap maps[2 * kMaxRanks];
+        const size_t size[4] = {(size_t)d->head_dim, (size_t)d->page_size, (size_t)d->kv_heads, d->pages};
+        const size_t strides[3] = {d->token_stride * 2, d->head_stride * 2, d->page_stride * 2};
+        const unsigned box[4] = {64, (unsigned)kv.box_tokens, 1, 1};
         for (int r = 0; r < h->n; ++r)
-            if (encode((PFN_cuTensorMapEncodeTiled_v12000)fn, &maps[r], *d, kv.box_tokens, k[r]) != CUDA_SUCCESS ||
-                encode((PFN_cuTensorMapEncodeTiled_v12000)fn, &maps[h->n + r], *d, kv.box_tokens, v[r]) != CUDA_SUCCESS)
+            if (encode_map(kv, &maps[r], 4, k[r], size, strides, box) != AR_OK ||
+                encode_map(kv, &maps[h->n + r], 4, v[r], size, strides, box) != AR_OK)
                 return AR_ERR_INVALID;
         const size_t floats = std::max(attention_decode_partial_floats(*h, d->head_dim),
                                        attention_chunk_partial_floats(*h, d->head_dim));

@@ -300,6 +300,16 @@ __device__ __forceinline__ void page_copy(void* smem_dst, const CUtensorMap* map
                  : "memory");
 }
 
+// One box of a packed [token][head][d] tensor.
+__device__ __forceinline__ void box_copy(void* smem_dst, const CUtensorMap* map, int d, int head, int token,
+                                         uint64_t* bar)
+{
+    asm volatile("cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+                 "[%0], [%1, {%2, %3, %4}], [%5];" ::"r"(smem_addr(smem_dst)),
+                 "l"(map), "r"(d), "r"(head), "r"(token), "r"(smem_addr(bar))
+                 : "memory");
+}
+
 __device__ __forceinline__ void prefetch_map(const CUtensorMap* map)
 {
     asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
