@@ -14,6 +14,9 @@
 //                   (a warp a half let them drift into step: 1364 for 1530 TFLOP/s)
 //   warp 9          tensor copies of K and V tiles (pages) into a ring of stages
 //   warp 10         tensor copies of the next rows' queries
+//   warp 11         waits for the tiles and tells warp 8 together with the probabilities:
+//                   issuing a product takes as long as the product, so every wait that
+//                   warp 8 does not need shortens the loop
 // The last four warps hand registers to the softmax warps, whose threads hold a
 // row of 128 scores.
 //
@@ -121,7 +124,7 @@ __device__ __forceinline__ bool next_segment(const BatchArgs& b, int tile_tokens
 // once a wait of the CTA has run out.
 __device__ __forceinline__ void warp_wait(bool& ok, uint64_t* bar, uint32_t parity, ChunkShared* sh, DevStatus* st)
 {
-    if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return;
+    if (__all_sync(0xffffffffu, mbar_wait_20us(bar, parity))) return;
     if (ok) ok = wait_or_give_up(bar, parity, &sh->gave_up, st);
     ok = __all_sync(0xffffffffu, ok);
 }
@@ -219,6 +222,61 @@ __device__ void load_queries(const ChunkArgs& a, const BatchArgs& b, uint8_t* q_
             if (in_flight[h]) wait_a_second(&sh->q_full[h], phase[h], nullptr);
 }
 
+// The tiles that the products of key tile i read beside the probabilities, V of
+// i and K of i + 1: once they are there, the last arrival on the first part's
+// barrier of each half that takes part.
+template <int D>
+__device__ void watch_tiles(const ChunkArgs& a, const BatchArgs& b, uint8_t* stages, ChunkShared* sh, DevStatus* st)
+{
+    const int lane = threadIdx.x & 31;
+    const Segment& seg = sh->seg[threadIdx.x / 32];
+    int stage = 0;
+    uint32_t phase = 0, p_phase[2] = {0, 0};
+    bool ok = true;
+    auto step = [&] {
+        if (++stage == kStages<D>) {
+            stage = 0;
+            phase ^= 1;
+        }
+    };
+    while (ok && next_segment(b, 2 * a.half_tokens, sh, st)) {
+        const int n[2] = {half_tile(a, seg, 0).tiles, half_tile(a, seg, 1).tiles};
+        const int tiles = max(n[0], n[1]), j0 = seg.j0, key_lo = seg.span.key_lo, key_hi = seg.span.key_hi;
+        if (tiles == 0) continue;
+        step();   // K of the first tile is warp 8's
+        for (int i = 0; ok && i < tiles; ++i) {
+            const int v_stage = stage;
+            warp_wait(ok, &sh->full[stage], phase, sh, st);
+            step();
+            if (i + 1 < tiles) {
+                warp_wait(ok, &sh->full[stage], phase, sh, st);
+                step();
+            }
+            const int key0 = (j0 + i) * kKeys;
+            if (key0 + kKeys > key_hi || key0 < key_lo) {
+                // slots of these pages that no row sees may hold anything: their values count as 0
+                const uint32_t base = smem_addr(stages + v_stage * kTileBytes<D>);
+                for (int x = lane; x < kKeys * (D / 8); x += 32) {
+                    const int r = x / (D / 8), c = x % (D / 8);
+                    if (key0 + r >= key_hi || key0 + r < key_lo) {
+                        const uint32_t at = base + (c >> 3) * (kKeys * 128) + r * 128 + (c & 7) * 16;
+                        asm volatile("st.shared.v4.b32 [%0], {%1,%1,%1,%1};" ::"r"(at), "r"(0) : "memory");
+                    }
+                }
+                fence_proxy_async();
+                __syncwarp();
+            }
+            for (int h = 0; h < 2; ++h)
+                if (i < n[h]) {
+                    // one phase at a time: not before the softmax warps' arrivals of the last
+                    warp_wait(ok, &sh->p_full[h][0], p_phase[h] ^ 1, sh, st);
+                    p_phase[h] ^= 1;
+                    if (lane == 0) mbar_arrive(&sh->p_full[h][0]);
+                }
+        }
+    }
+}
+
 template <int DT, int D>
 __device__ void issue(const ChunkArgs& a, const BatchArgs& b, uint8_t* q_tiles, uint8_t* stages, ChunkShared* sh,
                       DevStatus* st)
@@ -256,7 +314,7 @@ __device__ void issue(const ChunkArgs& a, const BatchArgs& b, uint8_t* q_tiles, 
     };
     while (ok && next_segment(b, 2 * a.half_tokens, sh, st)) {
         const int n[2] = {half_tile(a, seg, 0).tiles, half_tile(a, seg, 1).tiles};
-        const int tiles = max(n[0], n[1]), j0 = seg.j0, key_lo = seg.span.key_lo, key_hi = seg.span.key_hi;
+        const int tiles = max(n[0], n[1]);
         if (tiles == 0) continue;
         wait(&sh->full[stage], phase);
         for (int h = 0; h < 2; ++h)
@@ -271,29 +329,10 @@ __device__ void issue(const ChunkArgs& a, const BatchArgs& b, uint8_t* q_tiles, 
         step(stage, phase);
         for (int i = 0; ok && i < tiles; ++i) {
             const int v_stage = stage;
-            const uint32_t v_phase = phase;
             step(stage, phase);
             const int k_stage = stage;
-            const uint32_t k_phase = phase;
             const bool more = i + 1 < tiles;
             if (more) step(stage, phase);
-            // both tiles are waited for while the tensor cores still have the last tile's products
-            wait(&sh->full[v_stage], v_phase);
-            if (more) wait(&sh->full[k_stage], k_phase);
-            const int key0 = (j0 + i) * kKeys;
-            if (key0 + kKeys > key_hi || key0 < key_lo) {
-                // slots of these pages that no row sees may hold anything: their values count as 0
-                const uint32_t base = smem_addr(stages + v_stage * kTileBytes<D>);
-                for (int x = lane; x < kKeys * (D / 8); x += 32) {
-                    const int r = x / (D / 8), c = x % (D / 8);
-                    if (key0 + r >= key_hi || key0 + r < key_lo) {
-                        const uint32_t at = base + (c >> 3) * (kKeys * 128) + r * 128 + (c & 7) * 16;
-                        asm volatile("st.shared.v4.b32 [%0], {%1,%1,%1,%1};" ::"r"(at), "r"(0) : "memory");
-                    }
-                }
-                fence_proxy_async();
-                __syncwarp();
-            }
             for (int h = 0; h < 2; ++h) {
                 if (i >= n[h]) continue;
                 // the probabilities come in two parts: the product over the first 64 keys runs while
@@ -579,7 +618,7 @@ attention_chunk_kernel(const __grid_constant__ ChunkArgs a, const BatchArgs b, D
             mbar_init(&sh->q_full[h], 1);
             mbar_init(&sh->q_empty[h], 1);
             mbar_init(&sh->s_full[h], 1);
-            mbar_init(&sh->p_full[h][0], kHalf / 32);
+            mbar_init(&sh->p_full[h][0], kHalf / 32 + 1);
             mbar_init(&sh->p_full[h][1], kHalf / 32);
             mbar_init(&sh->o_full[h], 1);
         }
@@ -612,6 +651,8 @@ attention_chunk_kernel(const __grid_constant__ ChunkArgs a, const BatchArgs b, D
             produce<D>(a, b, stages, sh, st);
         else if (warp == 10)
             load_queries<D>(a, b, q_tiles, sh, st);
+        else
+            watch_tiles<D>(a, b, stages, sh, st);
     }
     pdl_release();
     tmem_before_sync();

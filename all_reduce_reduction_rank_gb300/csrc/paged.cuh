@@ -325,20 +325,27 @@ __device__ __forceinline__ void fence_proxy_async()
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
 }
 
-// Bounded wait: false after about a second.
+// Waits in the hardware, for about 20 us at most: a warp that polls takes issue
+// slots from the warps of its scheduler that compute.
+__device__ __forceinline__ bool mbar_wait_20us(uint64_t* bar, uint32_t parity)
+{
+    uint32_t done;
+    asm volatile("{\n\t.reg .pred p;\n\t"
+                 "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+                 "selp.u32 %0, 1, 0, p;\n\t}"
+                 : "=r"(done)
+                 : "r"(smem_addr(bar)), "r"(parity), "r"(20000u)
+                 : "memory");
+    return done != 0;
+}
+
+// Bounded wait: false after about a second (or once `stop` is set).
 __device__ __forceinline__ bool wait_a_second(uint64_t* bar, uint32_t parity, volatile int* stop)
 {
-    // the clock is read after 256 polls only: reading it costs as much as a tile's products
-    uint64_t t0 = 0;
+    const uint64_t t0 = globaltimer_ns();
     for (uint32_t i = 0; i < kMbarMaxPolls; ++i) {
-        if (mbar_try_wait(bar, parity)) return true;
-        if (stop && *stop) return false;
-        if ((i & 255) == 255) {
-            if (t0 == 0)
-                t0 = globaltimer_ns();
-            else if (globaltimer_ns() - t0 > 1000000000ull)
-                return false;
-        }
+        if (mbar_wait_20us(bar, parity)) return true;
+        if ((stop && *stop) || globaltimer_ns() - t0 > 1000000000ull) return false;
     }
     return false;
 }
@@ -347,6 +354,7 @@ __device__ __forceinline__ bool wait_a_second(uint64_t* bar, uint32_t parity, vo
 // once another warp has given up, and giving up sets the status word.
 __device__ __forceinline__ bool wait_or_give_up(uint64_t* bar, uint32_t parity, volatile int* gave_up, DevStatus* st)
 {
+    if (mbar_wait_20us(bar, parity)) return true;   // the usual end: the clock is not read
     if (wait_a_second(bar, parity, gave_up)) return true;
     *gave_up = 1;
     report_wait_timeout(st);
