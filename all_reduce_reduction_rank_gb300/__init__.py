@@ -189,7 +189,10 @@ def _addr(x) -> int | None:
 
 
 def _ptr_array(bufs) -> ctypes.Array:
-    return (ctypes.c_void_p * len(bufs))(*[_addr(b) for b in bufs])
+    try:   # the usual case, a list of tensors, without a call of our own per buffer
+        return (ctypes.c_void_p * len(bufs))(*[b.data_ptr() for b in bufs])
+    except AttributeError:
+        return (ctypes.c_void_p * len(bufs))(*[_addr(b) for b in bufs])
 
 
 def _stream(s) -> int | None:

@@ -90,7 +90,7 @@ int check_block_norm(int n, size_t max_bytes, const void* const* in, const ar_bl
     if (!(p->eps >= 0.0f) || p->eps == INFINITY || !std::isfinite(p->alpha) || !std::isfinite(p->beta))
         return AR_ERR_INVALID;
     const size_t e = elem_bytes(dt);
-    if (!block_norm_fits(hidden, dt)) return AR_ERR_INVALID;
+    if (hidden == 0 || hidden > kMaxNormHidden || hidden % (16u / e) != 0) return AR_ERR_INVALID;
     if (tokens > (size_t)INT_MAX / 16u || tokens > SIZE_MAX / hidden / 128u) return AR_ERR_TOO_LARGE;
     const size_t count = tokens * hidden;
     if (int rc = check_multi(AR_OP_ONE_SHOT, n, max_bytes, in, norm_out, count, dt)) return rc;
@@ -834,7 +834,9 @@ int ar_allreduce_block_norm(ar_handle hd, const void* const* in, const ar_block_
     h->timing.op = AR_OP_ALLREDUCE_BLOCK_NORM;
     if (count)
         rc = on_device(*h, [&] {
-            return launch_block_norm(*h, in, *p, norm_out, residual_out, tokens, hidden, dt, (cudaStream_t)stream);
+            const auto launch = dt == AR_F32 ? launch_block_norm_f32 : dt == AR_BF16 ? launch_block_norm_bf16
+                                                                                     : launch_block_norm_f16;
+            return launch(*h, in, *p, norm_out, residual_out, tokens, hidden, (cudaStream_t)stream);
         });
     if (rc != AR_OK) return rc;
     plan(AR_OP_ALLREDUCE_RMSNORM, h->n, count, dt, &h->last);   // the same rank, residual and output bytes

@@ -10,11 +10,15 @@
 // between the two means, so each byte moves once and the row's two sums are
 // the only waits.
 //
+// One source per payload type includes this (they compile side by side).
+//
 // Layout: a cluster of CL CTAs per token row, each with a contiguous slice of
 // it, VPT 16-byte vectors a thread.  Every warp sends its sum of squares into
 // every CTA of the cluster (distributed shared memory, counted on the
 // receiver's mbarrier), and every thread adds all of them in one order, so all
 // CTAs get the same bits; one barrier for each of the two sums.
+#pragma once
+
 #include "cluster.cuh"
 #include "layer.h"
 
@@ -149,75 +153,80 @@ block_norm_kernel(const __grid_constant__ CPtrs<NR> in, const NormArgs a, const 
     }
 }
 
-constexpr size_t kMaxHidden = 65536;
-
-}  // namespace
-
-bool block_norm_fits(size_t hidden, int dt)
+template <int DT>
+int launch_block_norm_as(Handle& h, const void* const* in, const ar_block_norm_t& p, void* const* out,
+                         void* residual_out, size_t tokens, size_t hidden, cudaStream_t s)
 {
-    return hidden > 0 && hidden <= kMaxHidden && hidden % (16u / elem_bytes(dt)) == 0;
-}
-
-int launch_block_norm(Handle& h, const void* const* in, const ar_block_norm_t& p, void* const* out,
-                      void* residual_out, size_t tokens, size_t hidden, int dt, cudaStream_t s)
-{
-    return dispatch_dtype(dt, [&](auto dtc) -> int {
-        constexpr int DT = decltype(dtc)::value;
-        return dispatch_ranks(h.n, [&](auto nrc) -> int {
-            constexpr int NR = decltype(nrc)::value;
-            CPtrs<NR> ip;
-            MPtrs<NR> op;
-            for (int q = 0; q < NR; ++q) {
-                ip.p[q] = in[q];
-                op.p[q] = out[q];
-            }
-            NormArgs a{p.residual, p.post_weight, p.gate, p.pre_weight, residual_out,
-                       p.gate ? p.gate_stride : 0, p.alpha, p.beta, p.eps};
-            const uint64_t e = sizeof(typename Payload<DT>::scalar_t);
-            const uint64_t S = (uint64_t)tokens * hidden * e, W = (uint64_t)hidden * e;
-            const uint64_t extra = (p.gate ? (p.gate_stride ? S : W) : 0) + W * (p.post_weight ? 2 : 1);
-            auto run = [&](auto clc, auto thc, auto vc) -> int {
-                constexpr int CL = decltype(clc)::value, TH = decltype(thc)::value, VPT = decltype(vc)::value;
-                auto kernel = block_norm_kernel<NR, DT, CL, TH, VPT>;
-                static std::atomic<uint32_t> attr_done{0};
-                if (CL > 8 && !once_per_device(attr_done, [&] {
-                        return cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) ==
-                               cudaSuccess;
-                    }))
-                    return AR_ERR_CUDA;
-                const unsigned slice = (unsigned)((hidden / kVecElems<DT> + CL - 1) / CL);
-                cudaLaunchAttribute attr[2];
-                attr[0].id = cudaLaunchAttributeClusterDimension;
-                attr[0].val.clusterDim.x = CL;
-                attr[0].val.clusterDim.y = 1;
-                attr[0].val.clusterDim.z = 1;
-                attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-                attr[1].val.programmaticStreamSerializationAllowed = h.pdl ? 1 : 0;
-                cudaLaunchConfig_t cfg{};
-                cfg.gridDim = dim3((unsigned)(tokens * CL));
-                cfg.blockDim = dim3(TH);
-                cfg.stream = s;
-                cfg.attrs = attr;
-                cfg.numAttrs = 2;
-                const int early = tokens * CL <= (size_t)h.sm_count ? 1 : 0;
-                rec_begin(h, s);
-                const cudaError_t err = cudaLaunchKernelEx(&cfg, kernel, ip, a, op, (unsigned)hidden, slice, early,
-                                                           h.status);
-                rec_end(h, s, AR_K_ALLREDUCE_BLOCK_NORM, 2ull * (NR + 1) * S + extra);
-                return err == cudaSuccess ? launch_status() : AR_ERR_CUDA;
-            };
-            using C8 = std::integral_constant<int, 8>;
-            using C16 = std::integral_constant<int, 16>;
-            using T128 = std::integral_constant<int, 128>;
-            using T256 = std::integral_constant<int, 256>;
-            using V1 = std::integral_constant<int, 1>;
-            using V4 = std::integral_constant<int, 4>;
-            const size_t nvec = hidden / kVecElems<DT>;
-            if (nvec <= 8 * 128) return run(C8{}, T128{}, V1{});
-            if (nvec <= 16 * 256) return run(C16{}, T256{}, V1{});
-            return run(C16{}, T256{}, V4{});
-        });
+    return dispatch_ranks(h.n, [&](auto nrc) -> int {
+        constexpr int NR = decltype(nrc)::value;
+        CPtrs<NR> ip;
+        MPtrs<NR> op;
+        for (int q = 0; q < NR; ++q) {
+            ip.p[q] = in[q];
+            op.p[q] = out[q];
+        }
+        NormArgs a{p.residual, p.post_weight, p.gate, p.pre_weight, residual_out,
+                   p.gate ? p.gate_stride : 0, p.alpha, p.beta, p.eps};
+        const uint64_t e = sizeof(typename Payload<DT>::scalar_t);
+        const uint64_t S = (uint64_t)tokens * hidden * e, W = (uint64_t)hidden * e;
+        const uint64_t extra = (p.gate ? (p.gate_stride ? S : W) : 0) + W * (p.post_weight ? 2 : 1);
+        auto run = [&](auto clc, auto thc, auto vc) -> int {
+            constexpr int CL = decltype(clc)::value, TH = decltype(thc)::value, VPT = decltype(vc)::value;
+            auto kernel = block_norm_kernel<NR, DT, CL, TH, VPT>;
+            static std::atomic<uint32_t> attr_done{0};
+            if (CL > 8 && !once_per_device(attr_done, [&] {
+                    return cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) ==
+                           cudaSuccess;
+                }))
+                return AR_ERR_CUDA;
+            const unsigned slice = (unsigned)((hidden / kVecElems<DT> + CL - 1) / CL);
+            cudaLaunchAttribute attr[2];
+            attr[0].id = cudaLaunchAttributeClusterDimension;
+            attr[0].val.clusterDim.x = CL;
+            attr[0].val.clusterDim.y = 1;
+            attr[0].val.clusterDim.z = 1;
+            attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+            attr[1].val.programmaticStreamSerializationAllowed = h.pdl ? 1 : 0;
+            cudaLaunchConfig_t cfg{};
+            cfg.gridDim = dim3((unsigned)(tokens * CL));
+            cfg.blockDim = dim3(TH);
+            cfg.stream = s;
+            cfg.attrs = attr;
+            cfg.numAttrs = 2;
+            const int early = tokens * CL <= (size_t)h.sm_count ? 1 : 0;
+            rec_begin(h, s);
+            const cudaError_t err = cudaLaunchKernelEx(&cfg, kernel, ip, a, op, (unsigned)hidden, slice, early,
+                                                       h.status);
+            rec_end(h, s, AR_K_ALLREDUCE_BLOCK_NORM, 2ull * (NR + 1) * S + extra);
+            return err == cudaSuccess ? launch_status() : AR_ERR_CUDA;
+        };
+        using C1 = std::integral_constant<int, 1>;
+        using C2 = std::integral_constant<int, 2>;
+        using C4 = std::integral_constant<int, 4>;
+        using C8 = std::integral_constant<int, 8>;
+        using C16 = std::integral_constant<int, 16>;
+        using T128 = std::integral_constant<int, 128>;
+        using T256 = std::integral_constant<int, 256>;
+        // Clusters just wide enough for one vector a thread of 128, so that a row's
+        // phases overlap another's on the same SM; up to 8 CTAs for rows too few to
+        // fill the SMs; two vectors a thread on 4 CTAs instead of one on 8 once the
+        // rows are many.  Swept on GB300 (n = 8 bf16, graph replay, every {1, 2, 4, 8,
+        // 16} CTAs x {64 ... 512} threads x {1, 2, 4} vectors): the best or within 4%
+        // of it at 1 x 4096 (2.1 us), 61 x 8192 (4.0), 128 x 4096 (3.9), 1000 x 512
+        // (4.5), 2000 x 1864 (25.4), 2000 x 4096 (50.3), 2000 x 16384 (201);
+        // 300 x 8192 (17.6; 16.5 with four vectors on 2 CTAs, which lose elsewhere).
+        // 4096 x 8192: 201 us with two vectors on 4 CTAs, 207 with one on 8.
+        const size_t nvec = hidden / kVecElems<DT>;
+        if (nvec <= 1024 && tokens * 8 <= (size_t)h.sm_count) return run(C8{}, T128{}, C1{});
+        if (nvec <= 128) return run(C1{}, T128{}, C1{});
+        if (nvec <= 256) return run(C2{}, T128{}, C1{});
+        if (nvec <= 512) return run(C4{}, T128{}, C1{});
+        if (nvec <= 1024) return tokens < 1024 ? run(C8{}, T128{}, C1{}) : run(C4{}, T128{}, C2{});
+        if (nvec <= 2048) return run(C8{}, T128{}, C2{});
+        if (nvec <= 4096) return run(C16{}, T128{}, C2{});
+        return run(C16{}, T256{}, C4{});
     });
 }
 
+}  // namespace
 }  // namespace argb

@@ -62,9 +62,13 @@ int encode_map(const KvCache& kv, CUtensorMap* map, int dims, const void* base, 
 
 Handle* handle_of(ar_handle h);      // nullptr if it is not a handle
 
-bool block_norm_fits(size_t hidden, int dt);
-int launch_block_norm(Handle& h, const void* const* in, const ar_block_norm_t& p, void* const* out,
-                      void* residual_out, size_t tokens, size_t hidden, int dt, cudaStream_t s);
+constexpr size_t kMaxNormHidden = 65536;   // 16 CTAs x 256 threads x 4 vectors of fp32
+int launch_block_norm_f32(Handle& h, const void* const* in, const ar_block_norm_t& p, void* const* out,
+                          void* residual_out, size_t tokens, size_t hidden, cudaStream_t s);
+int launch_block_norm_bf16(Handle& h, const void* const* in, const ar_block_norm_t& p, void* const* out,
+                           void* residual_out, size_t tokens, size_t hidden, cudaStream_t s);
+int launch_block_norm_f16(Handle& h, const void* const* in, const ar_block_norm_t& p, void* const* out,
+                          void* residual_out, size_t tokens, size_t hidden, cudaStream_t s);
 
 struct RopeCall {
     const void* const* q;            // nullptr: none
