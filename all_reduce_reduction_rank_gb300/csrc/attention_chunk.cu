@@ -684,21 +684,36 @@ attention_join_kernel(const __grid_constant__ ChunkArgs a)
     auto part_of = [&](unsigned k) {
         return a.partial + (size_t)part_slot(f, k) * kPartFloats<D> + h * (kHalf * (D + 2)) + row;
     };
-    float top = -INFINITY;
-#pragma unroll 8
-    for (unsigned k = 0; k < j.parts; ++k) top = fmaxf(top, __ldcg(part_of(k) + D * kHalf));
-    float o[kJoinColumns], sum = 0.0f;
+    // four parts at a time, all of their loads in flight at once; a later part with a larger
+    // maximum scales what is there
+    float top = -INFINITY, o[kJoinColumns], sum = 0.0f;
 #pragma unroll
     for (int e = 0; e < kJoinColumns; ++e) o[e] = 0.0f;
-#pragma unroll 4
-    for (unsigned k = 0; k < j.parts; ++k) {
-        const float* from = part_of(k);
-        const float m = __ldcg(from + D * kHalf);
-        if (m == -INFINITY) continue;   // a part that saw nothing wrote no columns
-        const float w = ex2(m - top);
-        sum = fmaf(__ldcg(from + (D + 1) * kHalf), w, sum);
+    for (unsigned k0 = 0; k0 < j.parts; k0 += 4) {
+        float m[4], l[4], x[4][kJoinColumns];
 #pragma unroll
-        for (int e = 0; e < kJoinColumns; ++e) o[e] = fmaf(__ldcg(from + (d + e) * kHalf), w, o[e]);
+        for (int k = 0; k < 4; ++k) {
+            const float* from = part_of(min(k0 + k, j.parts - 1));
+            m[k] = k0 + k < j.parts ? __ldcg(from + D * kHalf) : -INFINITY;
+            l[k] = __ldcg(from + (D + 1) * kHalf);
+#pragma unroll
+            for (int e = 0; e < kJoinColumns; ++e) x[k][e] = __ldcg(from + (d + e) * kHalf);
+        }
+        const float to = fmaxf(top, fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3])));
+        const float f = top == -INFINITY ? 0.0f : ex2(top - to);
+        top = to;
+        sum *= f;
+#pragma unroll
+        for (int e = 0; e < kJoinColumns; ++e) o[e] *= f;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            // a part that saw nothing wrote no columns: whatever is there does not count
+            const bool saw = m[k] != -INFINITY;
+            const float w = saw ? ex2(m[k] - to) : 0.0f;
+            sum = fmaf(saw ? l[k] : 0.0f, w, sum);
+#pragma unroll
+            for (int e = 0; e < kJoinColumns; ++e) o[e] = fmaf(saw ? x[k][e] : 0.0f, w, o[e]);
+        }
     }
     const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
     const int r = row + h * a.half_tokens * a.group;   // rows of half 0 come first

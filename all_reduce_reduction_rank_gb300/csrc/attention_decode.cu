@@ -42,6 +42,7 @@ template <int D> constexpr int kPartFloats = kRows * (D + 2);
 struct DecodeShared {
     uint64_t full[6], empty[6];
     float m[kWarps][kRows], l[kWarps][kRows];
+    float top[kRows], sum[kRows];
     SplitShared split;
     int gave_up, last;
 };
@@ -330,9 +331,18 @@ __device__ void consume(const DecodeArgs& a, const BatchArgs& b, const Cursor& c
         float f[2];
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-            float top = -INFINITY;
-            for (int w = 0; w < kWarps; ++w) top = fmaxf(top, sh->m[w][r0 + 8 * i]);
+            const int r = r0 + 8 * i;
+            float top = -INFINITY, sum = 0.0f;
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) top = fmaxf(top, sh->m[w][r]);
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w)
+                sum += sh->m[w][r] == -INFINITY ? 0.0f : sh->l[w][r] * ex2(sh->m[w][r] - top);
             f[i] = m[i] == -INFINITY ? 0.0f : ex2(m[i] - top);
+            if (warp == 0 && (lane & 3) == 0) {   // the barriers of the turns below publish them
+                sh->top[r] = top;
+                sh->sum[r] = sum;
+            }
         }
         float* mine = acc + (warp >> 1) * (kRows * D);
 #pragma unroll
@@ -367,10 +377,7 @@ __device__ void consume(const DecodeArgs& a, const BatchArgs& b, const Cursor& c
             const float4 x = *reinterpret_cast<const float4*>(acc + r * D + d);
             const float4 y = *reinterpret_cast<const float4*>(acc + kRows * D + r * D + d);
             float4 z = make_float4(x.x + y.x, x.y + y.y, x.z + y.z, x.w + y.w);
-            float top = -INFINITY, sum = 0.0f;
-            for (int w = 0; w < kWarps; ++w) top = fmaxf(top, sh->m[w][r]);
-            for (int w = 0; w < kWarps; ++w)
-                sum += sh->m[w][r] == -INFINITY ? 0.0f : sh->l[w][r] * ex2(sh->m[w][r] - top);
+            const float top = sh->top[r], sum = sh->sum[r];
             if (seg.parts == 1) {
                 const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
                 store_row4(r, d, make_float4(z.x * inv, z.y * inv, z.z * inv, z.w * inv));
@@ -383,34 +390,52 @@ __device__ void consume(const DecodeArgs& a, const BatchArgs& b, const Cursor& c
             }
         }
         if (seg.parts > 1) {
-            __threadfence();
+            // the barrier orders the other threads' stores before thread 0's release, and the last
+            // one's acquire before their loads
             consumers_sync();
             if (tid == 0) {
-                const unsigned before = atomicAdd(&a.arrived[seg.first_cta], 1u);
+                unsigned before;
+                asm volatile("atom.acq_rel.gpu.global.add.u32 %0, [%1], 1;"
+                             : "=r"(before)
+                             : "l"(&a.arrived[seg.first_cta])
+                             : "memory");
                 sh->last = before + 1 == seg.parts;
                 if (sh->last) a.arrived[seg.first_cta] = 0;   // for the next call
             }
             consumers_sync();
             if (sh->last) {
-                __threadfence();
                 for (int i = tid; i < rt.rows * (D / 4); i += 32 * kWarps) {
                     const int r = i / (D / 4), d = i % (D / 4) * 4;
-                    float top = -INFINITY;
-                    for (unsigned k = 0; k < seg.parts; ++k)
-                        top = fmaxf(top, __ldcg(a.partial + (size_t)part_slot(seg.first_cta, k) * kPartFloats<D> +
-                                                kRows * D + r));
+                    float top = -INFINITY, sum = 0.0f;
                     float4 z = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-                    float sum = 0.0f;
-                    for (unsigned k = 0; k < seg.parts; ++k) {
-                        const float* from = a.partial + (size_t)part_slot(seg.first_cta, k) * kPartFloats<D>;
-                        const float pm = __ldcg(from + kRows * D + r);
-                        const float w = pm == -INFINITY ? 0.0f : ex2(pm - top);
-                        const float4 x = __ldcg(reinterpret_cast<const float4*>(from + r * D + d));
-                        z.x = fmaf(x.x, w, z.x);
-                        z.y = fmaf(x.y, w, z.y);
-                        z.z = fmaf(x.z, w, z.z);
-                        z.w = fmaf(x.w, w, z.w);
-                        sum = fmaf(__ldcg(from + kRows * D + kRows + r), w, sum);
+                    // eight parts at a time, all of their loads in flight at once
+                    for (unsigned k0 = 0; k0 < seg.parts; k0 += 8) {
+                        float m[8], l[8];
+                        float4 x[8];
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) {
+                            const float* from =
+                                a.partial + (size_t)part_slot(seg.first_cta, min(k0 + k, seg.parts - 1)) * kPartFloats<D>;
+                            m[k] = k0 + k < seg.parts ? __ldcg(from + kRows * D + r) : -INFINITY;
+                            l[k] = __ldcg(from + kRows * D + kRows + r);
+                            x[k] = __ldcg(reinterpret_cast<const float4*>(from + r * D + d));
+                        }
+                        float to = top;
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) to = fmaxf(to, m[k]);
+                        const float f = top == -INFINITY ? 0.0f : ex2(top - to);
+                        top = to;
+                        sum *= f;
+                        z = make_float4(z.x * f, z.y * f, z.z * f, z.w * f);
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) {
+                            const float w = m[k] == -INFINITY ? 0.0f : ex2(m[k] - to);
+                            sum = fmaf(l[k], w, sum);
+                            z.x = fmaf(x[k].x, w, z.x);
+                            z.y = fmaf(x[k].y, w, z.y);
+                            z.z = fmaf(x[k].z, w, z.z);
+                            z.w = fmaf(x[k].w, w, z.w);
+                        }
                     }
                     const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
                     store_row4(r, d, make_float4(z.x * inv, z.y * inv, z.z * inv, z.w * inv));
