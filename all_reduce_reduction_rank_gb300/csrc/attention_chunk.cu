@@ -46,6 +46,7 @@ constexpr int kSoftmaxRegs = 208, kOtherRegs = 88;
 constexpr float kSlack = 8.0f;
 
 using ChunkSplit = Split<kKeys, 2, 5>;
+using ChunkWalk = Walk<ChunkSplit>;
 
 template <int D> constexpr int kTileBytes = kKeys * D * 2;    // of K, of V, and of a half's Q
 template <int D> constexpr int kStages = D == 128 ? 5 : 10;
@@ -59,7 +60,7 @@ struct ChunkShared {
     int gave_up;
     // each warp's place in the run: kept here, so that the loops over the keys
     // have the registers
-    Walk<ChunkSplit> walk[12];
+    ChunkWalk walk[12];
     Segment seg[12];
 };
 static_assert(sizeof(ChunkShared) <= 3072, "fits beside the tiles");
@@ -108,7 +109,7 @@ __device__ __forceinline__ HalfTile half_tile(const ChunkArgs& a, const Segment&
 __device__ __forceinline__ bool next_segment(const BatchArgs& b, int tile_tokens, ChunkShared* sh, DevStatus* st)
 {
     const int warp = threadIdx.x / 32;
-    Walk<ChunkSplit> walk = sh->walk[warp];
+    ChunkWalk walk = sh->walk[warp];
     Segment seg;
     const bool more = walk.next(b, tile_tokens, seg, st);
     __syncwarp();
@@ -631,11 +632,12 @@ attention_chunk_kernel(const __grid_constant__ ChunkArgs a, const BatchArgs b, D
     pdl_acquire();
     if (threadIdx.x == 0) a.joins[blockIdx.x].parts = 0;
     Cursor cur;
-    if (!split_work<ChunkSplit, kTh>(b, 2 * a.half_tokens, a.n * a.kv_heads, a.min_units, &sh->split, cur, st)) {
+    Seq at;
+    if (!split_work<ChunkSplit, kTh>(b, 2 * a.half_tokens, a.n * a.kv_heads, a.min_units, &sh->split, cur, at, st)) {
         pdl_release();
         return;
     }
-    if (threadIdx.x % 32 == 0) sh->walk[warp] = Walk<ChunkSplit>(cur);
+    if (threadIdx.x % 32 == 0) sh->walk[warp] = ChunkWalk(cur, at);
     if (warp == 8) tmem_alloc(&sh->tmem, 512);
     tmem_before_sync();
     __syncthreads();

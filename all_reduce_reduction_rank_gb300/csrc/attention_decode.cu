@@ -33,7 +33,7 @@ constexpr int kRows = 16;
 constexpr int kCtas = 2;                     // per SM
 constexpr float kSlack = 8.0f;               // log2 of how far p may pass 1
 
-using DecodeSplit = Split<kKeys, 0, 0>;
+using DecodeSplit = Split<kKeys, 1, 4>;
 
 template <int D> constexpr int kTileBytes = kKeys * D * 2;
 template <int D> constexpr int kStages = D == 128 ? 3 : 6;
@@ -62,6 +62,7 @@ struct DecodeArgs {
     int n, kv_heads, group;                  // query heads per kv head
     int tile_heads, head_groups, tm;         // query heads and new tokens of a row tile
     int box_tokens, min_units;
+    bool few;                                // split_few
 };
 
 template <int DT>
@@ -117,7 +118,7 @@ __device__ __forceinline__ RowTile row_tile(const DecodeArgs& a, const Segment& 
 }
 
 template <int D>
-__device__ void produce(const DecodeArgs& a, const BatchArgs& b, const Cursor& cur, uint8_t* stages, DecodeShared* sh,
+__device__ void produce(const DecodeArgs& a, const BatchArgs& b, const Cursor& cur, const Seq& at, uint8_t* stages, DecodeShared* sh,
                         DevStatus* st)
 {
     const int lane = threadIdx.x & 31;
@@ -126,7 +127,7 @@ __device__ void produce(const DecodeArgs& a, const BatchArgs& b, const Cursor& c
     // lane -> one copy of the tile
     const int box = lane % per_page, panel = (lane / per_page) % panels, is_v = lane / (per_page * panels);
     const bool mine = is_v < 2;
-    Walk<DecodeSplit> walk(cur);
+    Walk<DecodeSplit> walk(cur, at);
     Segment seg;
     int stage = 0;
     uint32_t phase = 0;
@@ -174,7 +175,7 @@ __device__ void produce(const DecodeArgs& a, const BatchArgs& b, const Cursor& c
 }
 
 template <int DT, int D>
-__device__ void consume(const DecodeArgs& a, const BatchArgs& b, const Cursor& cur, uint8_t* stages, float* acc,
+__device__ void consume(const DecodeArgs& a, const BatchArgs& b, const Cursor& cur, const Seq& at, uint8_t* stages, float* acc,
                         DecodeShared* sh, DevStatus* st)
 {
     using T = typename Payload<DT>::scalar_t;
@@ -182,7 +183,7 @@ __device__ void consume(const DecodeArgs& a, const BatchArgs& b, const Cursor& c
     constexpr int NT = D / 8;       // 8-wide column tiles of the output
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int r0 = lane >> 2, col = (lane & 3) * 2;
-    Walk<DecodeSplit> walk(cur);
+    Walk<DecodeSplit> walk(cur, at);
     Segment seg;
     int stage = 0;
     uint32_t phase = 0;
@@ -464,15 +465,20 @@ attention_decode_kernel(const __grid_constant__ DecodeArgs a, const BatchArgs b,
     // written by the host when the caches were registered: no need to wait for the launch before
     if (threadIdx.x < 2 * a.n) prefetch_map(a.maps + threadIdx.x);
     pdl_acquire();
+    __syncthreads();   // the ring's barriers are set up
     Cursor cur;
-    if (!split_work<DecodeSplit, kTh>(b, a.tm, a.n * a.kv_heads * a.head_groups, a.min_units, &sh->split, cur, st)) {
+    Seq at;
+    const int heads = a.n * a.kv_heads * a.head_groups;
+    const bool some = a.few ? split_few<DecodeSplit>(b, a.tm, heads, a.min_units, cur, at, st)
+                            : split_work<DecodeSplit, kTh>(b, a.tm, heads, a.min_units, &sh->split, cur, at, st);
+    if (!some) {
         pdl_release();
         return;
     }
     if (threadIdx.x >= 32 * kWarps)
-        produce<D>(a, b, cur, smem, sh, st);
+        produce<D>(a, b, cur, at, smem, sh, st);
     else
-        consume<DT, D>(a, b, cur, smem, acc, sh, st);
+        consume<DT, D>(a, b, cur, at, smem, acc, sh, st);
     pdl_release();
 }
 
@@ -507,6 +513,7 @@ int launch_attention_decode(KvCache& kv, const ar_batch_t& b, const AttnCall& c,
     a.tm = kRows / a.tile_heads;
     a.box_tokens = kv.box_tokens;
     a.min_units = 2;
+    a.few = b.seqs <= 256 && (b.max_new + a.tm - 1) / a.tm <= 8;
     const uint64_t moved = (uint64_t)h.n * b.tokens * c.q_heads * kv.d.head_dim * 2u * 2u;
     auto run = [&](auto dtc, auto dc) -> int {
         constexpr int DT = decltype(dtc)::value, D = decltype(dc)::value;

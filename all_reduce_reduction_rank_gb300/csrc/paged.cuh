@@ -104,10 +104,114 @@ struct SplitShared {
     int s;
 };
 
+// Where a run begins, from the units before its triple's sequence (`off`: the
+// run's first unit within that sequence).  Every warp walks the sequence's row
+// tiles, 32 at a time.
+template <typename S>
+__device__ __forceinline__ void enter_sequence(const BatchArgs& b, int tm, const Seq& q, u64 g, u64 off, Cursor& c)
+{
+    const int lane = threadIdx.x & 31;
+    auto units_of = [&](int t) { return (unsigned)(span_of<S::KT>(q, tm, t, b.window).tiles + S::W); };
+    const int nt = (q.nq + tm - 1) / tm;
+    c.t = 0;
+    for (int t0 = 0; nt > 1; t0 += 32) {
+        const int t = t0 + lane;
+        const u64 u = t < nt ? units_of(t) : 0;
+        u64 in = u;
+        for (int o = 1; o < 32; o <<= 1) {
+            const u64 x = __shfl_up_sync(0xffffffffu, in, o);
+            if (lane >= o) in += x;
+        }
+        const unsigned here = __ballot_sync(0xffffffffu, in > off);
+        if (here) {
+            const int src = __ffs(here) - 1;
+            c.t = t0 + src;
+            off -= __shfl_sync(0xffffffffu, in - u, src);
+            break;
+        }
+        if (t0 + 32 >= nt) break;   // not reached: the tiles' units cover `off`
+        off -= __shfl_sync(0xffffffffu, in, 31);
+    }
+    c.begin = g - off;
+    const int units = (int)units_of(c.t), o = (int)off, snap = min(c.snap, units / 2);
+    c.tile = o <= snap ? 0 : units - o <= snap ? units - S::W : o - S::W;
+}
+
+// The runs, from the units of one head group; false for a CTA without one.
+template <typename S>
+__device__ __forceinline__ bool cut_runs(u64 per_head, int heads, int min_units, Cursor& c, u64& g, u64& in_head)
+{
+    c.total = per_head * (unsigned)heads;
+    c.ctas = gridDim.x;
+    const u64 most = quotient(c.total + min_units - 1, min_units);
+    if (most < c.ctas) c.ctas = (unsigned)most;
+    if (blockIdx.x >= c.ctas) return false;
+    g = run_begin(c.total, c.ctas, blockIdx.x);
+    c.end = run_begin(c.total, c.ctas, blockIdx.x + 1);
+    if (S::SNAP > 0) {
+        const u64 eighth = quotient(c.total, c.ctas) / 8;
+        c.snap = eighth < (u64)S::W ? S::W : eighth > (u64)S::SNAP ? S::SNAP : (int)eighth;
+    } else {
+        c.snap = 0;
+    }
+    c.head = (int)quotient(g, per_head);
+    in_head = g - c.head * per_head;
+    return true;
+}
+
+// split_work for at most 256 sequences of few row tiles each (decode steps):
+// every warp goes over all of them by itself, without shared memory, barriers
+// and second loads (1.9 us of a decode step's 10 went into the other form).
+template <typename S>
+__device__ bool split_few(const BatchArgs& b, int tm, int heads, int min_units, Cursor& c, Seq& at, DevStatus* st)
+{
+    const int lane = threadIdx.x & 31;
+    const int per = (b.seqs + 31) / 32, s0 = min(lane * per, b.seqs), s1 = min(s0 + per, b.seqs);
+    auto units_in = [&](const Seq& q) {
+        unsigned sum = 0;
+        const int nt = (q.nq + tm - 1) / tm;
+        for (int t = 0; t < nt; ++t) sum += (unsigned)(span_of<S::KT>(q, tm, t, b.window).tiles + S::W);
+        return sum;
+    };
+    u64 mine = 0;
+    Seq q{0, 0, 0, 0};
+#pragma unroll 4
+    for (int s = s0; s < s1; ++s) {
+        q = load_seq(b, s, st);
+        mine += units_in(q);
+    }
+    u64 incl = mine;
+    for (int o = 1; o < 32; o <<= 1) {
+        const u64 x = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += x;
+    }
+    u64 g, in_head;
+    if (!cut_runs<S>(__shfl_sync(0xffffffffu, incl, 31), heads, min_units, c, g, in_head)) return false;
+    const int src = __ffs(__ballot_sync(0xffffffffu, in_head < incl)) - 1;
+    u64 off = in_head - (incl - mine);   // of lane src; the others' is not used
+    int s = s0;
+    if (per > 1 && lane == src)
+        for (;; ++s) {
+            q = load_seq(b, s, st);
+            const unsigned u = units_in(q);
+            if (off < u) break;
+            off -= u;
+        }
+    c.s = __shfl_sync(0xffffffffu, s, src);
+    off = __shfl_sync(0xffffffffu, off, src);
+    at.q0 = __shfl_sync(0xffffffffu, q.q0, src);
+    at.nq = __shfl_sync(0xffffffffu, q.nq, src);
+    at.len = __shfl_sync(0xffffffffu, q.len, src);
+    at.c0 = __shfl_sync(0xffffffffu, q.c0, src);
+    enter_sequence<S>(b, tm, at, g, off, c);
+    return true;
+}
+
 // Called by all NT threads; false for a CTA with nothing to do.  `min_units`:
-// a run is at least that long, so that small calls do not pay for joins.
+// a run is at least that long, so that small calls do not pay for joins.  `at`:
+// the sequence the run begins in.
 template <typename S, int NT>
-__device__ bool split_work(const BatchArgs& b, int tm, int heads, int min_units, SplitShared* sh, Cursor& c,
+__device__ bool split_work(const BatchArgs& b, int tm, int heads, int min_units, SplitShared* sh, Cursor& c, Seq& at,
                            DevStatus* st)
 {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -155,17 +259,8 @@ __device__ bool split_work(const BatchArgs& b, int tm, int heads, int min_units,
         if (w < warp) before += sh->warp_sum[w];
         per_head += sh->warp_sum[w];
     }
-    c.total = per_head * (unsigned)heads;
-    c.ctas = gridDim.x;
-    const u64 most = (c.total + min_units - 1) / min_units;
-    if (most < c.ctas) c.ctas = (unsigned)most;
-    if (blockIdx.x >= c.ctas) return false;   // the whole CTA
-    const u64 g = run_begin(c.total, c.ctas, blockIdx.x);
-    c.end = run_begin(c.total, c.ctas, blockIdx.x + 1);
-    const u64 eighth = quotient(c.total, c.ctas) / 8;
-    c.snap = eighth < (u64)S::W ? S::W : eighth > (u64)S::SNAP ? S::SNAP : (int)eighth;
-    c.head = (int)quotient(g, per_head);
-    const u64 in_head = g - c.head * per_head;
+    u64 g, in_head;
+    if (!cut_runs<S>(per_head, heads, min_units, c, g, in_head)) return false;   // the whole CTA
     const u64 excl = before + incl - mine;
     if (in_head >= excl && in_head < excl + mine) {   // (false without sequences: mine is 0)
         // this thread's sequences hold it
@@ -187,32 +282,8 @@ __device__ bool split_work(const BatchArgs& b, int tm, int heads, int min_units,
     }
     __syncthreads();
     c.s = sh->s;
-    // the row tile inside the sequence: every warp walks it, 32 tiles at a time
-    u64 off = sh->off;
-    const Seq q = load_seq(b, c.s, st);
-    const int nt = (q.nq + tm - 1) / tm;
-    c.t = 0;
-    for (int t0 = 0; nt > 1; t0 += 32) {
-        const int t = t0 + lane;
-        const u64 u = t < nt ? units_of(q, t) : 0;
-        u64 in = u;
-        for (int o = 1; o < 32; o <<= 1) {
-            const u64 x = __shfl_up_sync(0xffffffffu, in, o);
-            if (lane >= o) in += x;
-        }
-        const unsigned here = __ballot_sync(0xffffffffu, in > off);
-        if (here) {
-            const int src = __ffs(here) - 1;
-            c.t = t0 + src;
-            off -= __shfl_sync(0xffffffffu, in - u, src);
-            break;
-        }
-        if (t0 + 32 >= nt) break;   // not reached: the tiles' units cover `off`
-        off -= __shfl_sync(0xffffffffu, in, 31);
-    }
-    c.begin = g - off;
-    const int units = (int)units_of(q, c.t), o = (int)off, snap = min(c.snap, units / 2);
-    c.tile = o <= snap ? 0 : units - o <= snap ? units - S::W : o - S::W;
+    at = load_seq(b, c.s, st);
+    enter_sequence<S>(b, tm, at, g, sh->off, c);
     return true;
 }
 
@@ -233,7 +304,7 @@ struct Walk {
     int loaded;
 
     Walk() = default;   // in shared memory
-    __device__ __forceinline__ explicit Walk(const Cursor& cur) : c(cur), q{0, 0, 0, 0}, loaded(-1) {}
+    __device__ __forceinline__ Walk(const Cursor& cur, const Seq& at) : c(cur), q(at), loaded(cur.s) {}
 
     __device__ __forceinline__ bool next(const BatchArgs& b, int tm, Segment& seg, DevStatus* st)
     {
