@@ -109,6 +109,8 @@ _lib = None
 def lib() -> ctypes.CDLL:
     """Load libar_gb300.so from the package directory (raises if it is not built)."""
     global _lib
+    if _lib is not None:   # every call comes through here
+        return _lib
     with _lock:
         if _lib is None:
             if not LIB_PATH.exists():
