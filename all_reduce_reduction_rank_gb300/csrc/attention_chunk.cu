@@ -41,8 +41,8 @@ namespace {
 constexpr int kKeys = 128;
 constexpr int kHalf = kAttnTileRows;        // rows of a half
 constexpr int kTh = 384;
-// Registers a thread: 384 x 168 at launch = 256 x 208 + 128 x 88.
-constexpr int kSoftmaxRegs = 208, kOtherRegs = 88;
+// Registers a thread: 384 x 168 at launch = 256 x 200 + 128 x 104.
+constexpr int kSoftmaxRegs = 200, kOtherRegs = 104;
 constexpr float kSlack = 8.0f;
 
 using ChunkSplit = Split<kKeys, 2, 5>;

@@ -18,23 +18,33 @@ struct Seq {
     int q0, nq, len, c0;
 };
 
+struct RawSeq {
+    int q0, q1, len;
+};
+
+__device__ __forceinline__ RawSeq read_seq(const BatchArgs& b, int s)
+{
+    return RawSeq{b.q_start[s], b.q_start[s + 1], b.kv_len[s]};
+}
+
 // Values out of range reach no memory: a bad token range counts as no tokens,
 // a bad length as no keys.
-__device__ __forceinline__ Seq load_seq(const BatchArgs& b, int s, DevStatus* st)
+__device__ __forceinline__ Seq check_seq(const BatchArgs& b, const RawSeq& x, DevStatus* st)
 {
-    const int q0 = b.q_start[s], q1 = b.q_start[s + 1], len = b.kv_len[s];
-    Seq r{q0, q1 - q0, len, 0};
-    if (q0 < 0 || q1 < q0 || q1 > b.tokens) {
+    Seq r{x.q0, x.q1 - x.q0, x.len, 0};
+    if (x.q0 < 0 || x.q1 < x.q0 || x.q1 > b.tokens) {
         report_index(st);
         r.q0 = r.nq = 0;
     }
-    if (len < 0 || len > (1 << 30) || (size_t)len > (b.table_stride << b.page_shift)) {
+    if (x.len < 0 || x.len > (1 << 30) || (size_t)x.len > (b.table_stride << b.page_shift)) {
         report_index(st);
         r.len = 0;
     }
     r.c0 = r.len - r.nq;
     return r;
 }
+
+__device__ __forceinline__ Seq load_seq(const BatchArgs& b, int s, DevStatus* st) { return check_seq(b, read_seq(b, s), st); }
 
 // ---- split of the work ------------------------------------------------------------
 // A row tile is TM consecutive new tokens of a sequence with the query heads of
@@ -175,10 +185,22 @@ __device__ bool split_few(const BatchArgs& b, int tm, int heads, int min_units, 
     };
     u64 mine = 0;
     Seq q{0, 0, 0, 0};
-#pragma unroll 4
-    for (int s = s0; s < s1; ++s) {
-        q = load_seq(b, s, st);
-        mine += units_in(q);
+    if (per == 1) {
+        if (s0 < s1) {
+            q = load_seq(b, s0, st);
+            mine = units_in(q);
+        }
+    } else {
+        RawSeq raw[8];   // all loads before the first use: a report orders what follows it
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+            if (s0 + k < s1) raw[k] = read_seq(b, s0 + k);
+#pragma unroll 1
+        for (int k = 0; k < per; ++k) {
+            if (s0 + k < s1) mine += units_in(check_seq(b, raw[0], st));
+#pragma unroll
+            for (int i = 0; i < 7; ++i) raw[i] = raw[i + 1];
+        }
     }
     u64 incl = mine;
     for (int o = 1; o < 32; o <<= 1) {
