@@ -629,7 +629,7 @@ attention_chunk_kernel(const __grid_constant__ ChunkArgs a, const BatchArgs b, D
     }
     // written by the host when the caches were registered: no need to wait for the launch before
     if (threadIdx.x < 2 * a.n) prefetch_map(a.maps + threadIdx.x);
-    pdl_acquire();
+    pdl_acquire_for_copies();
     if (threadIdx.x == 0) a.joins[blockIdx.x].parts = 0;
     Cursor cur;
     Seq at;

@@ -464,7 +464,7 @@ attention_decode_kernel(const __grid_constant__ DecodeArgs a, const BatchArgs b,
     }
     // written by the host when the caches were registered: no need to wait for the launch before
     if (threadIdx.x < 2 * a.n) prefetch_map(a.maps + threadIdx.x);
-    pdl_acquire();
+    pdl_acquire_for_copies();
     __syncthreads();   // the ring's barriers are set up
     Cursor cur;
     Seq at;

@@ -319,8 +319,12 @@ int ar_paged_attention(ar_kv k, const ar_batch_t* b, const void* const* q, void*
     const size_t row = (size_t)kv->d.head_dim * (size_t)q_heads;
     int rc = AR_OK;
     h.timing.op = AR_OP_PAGED_ATTENTION;
-    // rows of a sequence per kv head: the decode kernel's tile holds 16
-    const bool few = (size_t)b->max_new * (size_t)(q_heads / kv->d.kv_heads) <= 16u || b->max_new == 1;
+    // Rows of a sequence per kv head.  The decode kernel reads the keys again for every 16 of
+    // them, the chunk kernel computes 256 whatever there is.  Measured on GB300 (n = 4, 2 kv heads,
+    // 64 sequences of 2000 keys, us, decode / chunk): heads of 128, 16 rows 94 / 116, 32 rows
+    // 167 / 117; heads of 64, 32 rows 91 / 96, 64 rows 165 / 96.
+    const size_t rows = (size_t)b->max_new * (size_t)(q_heads / kv->d.kv_heads);
+    const bool few = rows <= (kv->d.head_dim == 64 ? 32u : 16u);
     if (b->tokens)
         rc = on_device_of(h, [&] {
             return few ? launch_attention_decode(*kv, *b, c, window, (cudaStream_t)stream)

@@ -418,6 +418,14 @@ __device__ __forceinline__ void fence_proxy_async()
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
 }
 
+// pdl_acquire for kernels whose tensor copies read what the launch before wrote
+// with ordinary stores (the queries, the caches' new slots).
+__device__ __forceinline__ void pdl_acquire_for_copies()
+{
+    pdl_acquire();
+    asm volatile("fence.proxy.async.global;" ::: "memory");
+}
+
 // Waits in the hardware, for about 20 us at most: a warp that polls takes issue
 // slots from the warps of its scheduler that compute.
 __device__ __forceinline__ bool mbar_wait_20us(uint64_t* bar, uint32_t parity)
