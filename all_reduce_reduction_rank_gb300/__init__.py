@@ -190,11 +190,15 @@ def _addr(x) -> int | None:
     return int(x.data_ptr())  # torch.Tensor
 
 
+_POINTERS = {n: ctypes.c_void_p * n for n in range(17)}
+
+
 def _ptr_array(bufs) -> ctypes.Array:
+    array = _POINTERS.get(len(bufs)) or ctypes.c_void_p * len(bufs)
     try:   # the usual case, a list of tensors, without a call of our own per buffer
-        return (ctypes.c_void_p * len(bufs))(*[b.data_ptr() for b in bufs])
+        return array(*[b.data_ptr() for b in bufs])
     except AttributeError:
-        return (ctypes.c_void_p * len(bufs))(*[_addr(b) for b in bufs])
+        return array(*[_addr(b) for b in bufs])
 
 
 def _stream(s) -> int | None:

@@ -45,7 +45,7 @@ constexpr int kTh = 384;
 constexpr int kSoftmaxRegs = 200, kOtherRegs = 104;
 constexpr float kSlack = 8.0f;
 
-using ChunkSplit = Split<kKeys, 2, 5>;
+using ChunkSplit = Split<kKeys, 3, 5>;
 using ChunkWalk = Walk<ChunkSplit>;
 
 template <int D> constexpr int kTileBytes = kKeys * D * 2;    // of K, of V, and of a half's Q

@@ -92,6 +92,13 @@ def test_many_sequences_and_heads():
     check(2, 40, 3, 64, 32, "bf16", new, kv, 64, 0)
 
 
+@pytest.mark.parametrize("q_heads,kv_heads,dim,R,interleaved", [(7, 1, 64, 32, 1), (4, 2, 128, 128, 0), (40, 3, 128, 64, 0),
+                                                               (1, 1, 64, 64, 1), (70, 2, 64, 48, 0)])
+def test_many_tokens(q_heads, kv_heads, dim, R, interleaved):
+    # over 1024 tokens x ranks: 4 heads a thread, up to 4 tokens a CTA, or several CTAs a token
+    check(2, q_heads, kv_heads, dim, 64, "bf16", [301, 1, 0, 250], [301, 77, 5, 400], R, interleaved, pad=8)
+
+
 def test_another_stream():
     s = torch.cuda.Stream()
     check(2, 2, 1, 64, 16, "bf16", [2], [9], 64, 0, stream=s)
