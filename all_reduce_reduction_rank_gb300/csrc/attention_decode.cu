@@ -12,6 +12,14 @@
 // every tile with their own running maximum, sum and output accumulators, so
 // nothing but the ring's barriers is shared until a row tile's keys end.
 //
+// Measured on GB300 (n = 8 bf16, heads of 128, 8 query heads a kv head): 64
+// sequences of 1 to 8192 keys, 792 MB: 130 us, 6.1 TB/s (91% of the copy rate); 4
+// sequences of 70 to 131 thousand keys (n = 4 fp16, 1.77 GB): 266 us, 6.65 TB/s
+// (100%); one sequence of 1500 keys: 9.9 us, where launch, split, page, copy, two
+// tiles and the join follow one another.  Short sequences are bound by the same
+// chain per row tile, about 3.5 us (64 sequences of 300 keys: 29 us for 12.5 us of
+// bytes); the tensor pipe is 17% busy.
+//
 // Softmax in one pass, base 2: with x = scale log2(e) (q . k), a running
 // reference m, p = 2^(x - m), l = sum p, o = sum p v.  m moves only when a row's
 // maximum passes it by more than 8: p stays below 2^8, which fp32 sums, fp16
@@ -33,6 +41,8 @@ constexpr int kRows = 16;
 constexpr int kCtas = 2;                     // per SM
 constexpr float kSlack = 8.0f;               // log2 of how far p may pass 1
 
+// a row tile's start and end weigh a key tile more (0 / 1 / 2 / 3: 8 sequences of 700
+// keys 15.1 / 12.6 / 13.4 / 14.1 us, 64 of 1000 keys 59 / 55.5 / 53.5 / 53.0)
 using DecodeSplit = Split<kKeys, 1, 4>;
 
 template <int D> constexpr int kTileBytes = kKeys * D * 2;

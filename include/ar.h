@@ -512,7 +512,7 @@ typedef struct {
 /* Register the n_ranks caches of a handle: k and v are host arrays of n_ranks
  * device pointers (16-byte aligned; the caller keeps the memory).  Builds the
  * copies' descriptors and allocates the attention's workspace (partial results
- * of rows whose keys are split over several CTAs, about 85 MB) once; no later
+ * of rows whose keys are split over several CTAs, about 40 MB) once; no later
  * call allocates.  Calls on one ar_kv share that workspace: order them on one
  * stream or with events.  Destroy it before its handle.  *out is set only on
  * AR_OK. */
@@ -578,6 +578,12 @@ int ar_rope_append(ar_kv kv, const ar_batch_t* batch, const void* const* q, cons
  * A non-finite value within them may reach every row of the sequence.
  * Scores, softmax statistics and sums are fp32; the probabilities are rounded
  * to the cache's type before they meet the values, the output once at the end.
+ * Few rows per kv head (max_new x q_heads / kv_heads up to 16, 32 for heads of
+ * 64) and more take different kernels; either is right for every batch, and the
+ * result does not depend on how the keys are split over the CTAs in between (the
+ * split follows the batch alone, and its parts are joined in one order).
+ * ar_traffic reports the queries' and outputs' bytes: the keys are known on the
+ * device only.
  * q_heads is a multiple of kv_heads, at most 64 times it; scale is finite and > 0. */
 int ar_paged_attention(ar_kv kv, const ar_batch_t* batch, const void* const* q, void* const* out, int q_heads,
                        size_t q_stride, size_t out_stride, float scale, int window, ar_stream_t stream);

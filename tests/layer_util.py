@@ -27,12 +27,16 @@ class Layer:
         dt = TORCH[dtype]
         per = [-(-max(x, 0) // page) for x in kv]
         self.pages = pages or sum(per) + spare
-        shape = (self.pages, kv_heads, page, dim) if order == "head" else (self.pages, page, kv_heads, dim)
-        nan = lambda: torch.full(shape, float("nan"), dtype=dt, device="cuda")
-        self.k, self.v = [nan() for _ in range(n)], [nan() for _ in range(n)]
+        shape = (self.pages, page, kv_heads, dim) if order == "slot" else (self.pages, kv_heads, page, dim)
+        nan = lambda *s: torch.full(s, float("nan"), dtype=dt, device="cuda")
+        if order == "pair":     # keys and values of a page side by side in one allocation
+            both = [nan(self.pages, 2, *shape[1:]) for _ in range(n)]
+            self.k, self.v = [t[:, 0] for t in both], [t[:, 1] for t in both]
+        else:
+            self.k, self.v = [nan(*shape) for _ in range(n)], [nan(*shape) for _ in range(n)]
         st = self.k[0].stride()
-        self.strides = (st[0], st[1], st[2]) if order == "head" else (st[0], st[2], st[1])
-        head = lambda c: c if order == "head" else c.transpose(1, 2)    # [page, head, slot, dim] views
+        self.strides = (st[0], st[2], st[1]) if order == "slot" else (st[0], st[1], st[2])
+        head = lambda c: c.transpose(1, 2) if order == "slot" else c    # [page, head, slot, dim] views
         self.kview, self.vview = [head(c) for c in self.k], [head(c) for c in self.v]
         ids = (torch.randperm(self.pages - low, generator=g) + low)[: sum(per)].tolist()
         self.width = max(1, max(per, default=1)) + 1

@@ -63,6 +63,7 @@ def check(n, kv_heads, group, dim, page, dtype, new, kv, *, window=0, seed=0, **
     first = None
     if window:
         first = [max(0, x - q - window + 1) for q, x in zip(new, kv)]
+        first = [min(max(0, f), max(0, x)) for f, x in zip(first, kv)]
     with Layer(n, kv_heads, dim, page, dtype, new, kv, seed=seed, first_kept=first, **k) as L:
         q, out = run(L, kv_heads * group, window=window, **strides)
         compare(L, q, out, kv_heads * group, L.dim**-0.5, window)
@@ -116,6 +117,41 @@ def test_rows_that_see_nothing_are_zero(max_new):
 @pytest.mark.parametrize("new,kv", [([1, 1, 1], [40, 1000, 129]), ([70, 1, 9], [200, 300, 9])])
 def test_either_kernel_gives_the_definition(max_new, new, kv):
     check(2, 2, 5, 128, 64, "f16", new, kv, max_new=max_new)
+
+
+@pytest.mark.parametrize("max_new", [1, 500])
+def test_keys_and_values_in_one_allocation(max_new):
+    check(2, 3, 4, 64, 32, "bf16", [1, 30, 2], [100, 45, 64], order="pair", max_new=max_new)
+
+
+@pytest.mark.parametrize("seed", range(12))
+@pytest.mark.parametrize("max_new", [1, 500])
+def test_random_batches(seed, max_new):
+    rng = np.random.default_rng(seed)
+    pick = lambda *xs: xs[int(rng.integers(len(xs)))]
+    seqs = int(rng.integers(1, 12))
+    new = [int(x) for x in rng.integers(0, pick(3, 40, 150), seqs)]
+    kv = [max(0, int(q + x - pick(0, 0, 3))) for q, x in zip(new, rng.integers(0, pick(5, 300, 900), seqs))]
+    if sum(new) == 0:
+        new[0], kv[0] = 1, kv[0] + 1
+    check(int(rng.integers(2, 5)), pick(1, 2), pick(1, 2, 4, 6, 7), pick(64, 128), pick(16, 32, 64, 128),
+          pick("bf16", "f16"), new, kv, window=pick(0, 0, int(rng.integers(1, 200))), order=pick("head", "slot", "pair"),
+          max_new=max_new, seed=seed)
+
+
+@pytest.mark.parametrize("max_new", [1, 500])
+def test_chains_without_programmatic_launch(max_new):
+    with Layer(2, 1, 128, 16, "bf16", [1, 50], [700, 90], max_new=max_new) as L:
+        assert ar.ar_set_option(L.h, ar.AR_OPT_PDL, 0) == ar.AR_OK
+        q, out = run(L, 4)
+        compare(L, q, out, 4, L.dim**-0.5, 0)
+        with_pdl = [o.clone() for o in out]
+        assert ar.ar_set_option(L.h, ar.AR_OPT_PDL, 1) == ar.AR_OK
+        for _ in range(5):   # back to back: each call finds the last one's workspace in use or free
+            ar.check(ar.ar_paged_attention(L.handle, L.batch, q, out, 4, 512, 512, L.dim**-0.5, 0))
+        assert ar.ar_status(L.h) == ar.AR_OK
+        for x, y in zip(out, with_pdl):
+            assert torch.equal(x[: L.tokens], y[: L.tokens])
 
 
 def test_many_sequences():

@@ -75,7 +75,7 @@ def test_rotations(dim, R, interleaved, dtype):
 
 
 @pytest.mark.parametrize("page", [16, 32, 64, 128])
-@pytest.mark.parametrize("order", ["head", "slot"])
+@pytest.mark.parametrize("order", ["head", "slot", "pair"])
 def test_pages_and_orders(page, order):
     check(3, 4, 1, 128, page, "bf16", [1, 70, 1], [1, 200, 129], 128, 0, order=order, pad=8)
 
