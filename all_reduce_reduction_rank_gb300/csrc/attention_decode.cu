@@ -15,10 +15,10 @@
 // Measured on GB300 (n = 8 bf16, heads of 128, 8 query heads a kv head): 64
 // sequences of 1 to 8192 keys, 792 MB: 130 us, 6.1 TB/s (91% of the copy rate); 4
 // sequences of 70 to 131 thousand keys (n = 4 fp16, 1.77 GB): 266 us, 6.65 TB/s
-// (100%); one sequence of 1500 keys: 9.9 us, where launch, split, page, copy, two
+// (100%); one sequence of 1500 keys: 9.7 us, where launch, split, page, copy, two
 // tiles and the join follow one another.  Short sequences are bound by the same
-// chain per row tile, about 3.5 us (64 sequences of 300 keys: 29 us for 12.5 us of
-// bytes); the tensor pipe is 17% busy.
+// chain per row tile, about 3.5 us (64 sequences of 300 keys: 28 us for 12.5 us of
+// bytes); the tensor pipe is 17% busy, the warps wait for one another's results.
 //
 // Softmax in one pass, base 2: with x = scale log2(e) (q . k), a running
 // reference m, p = 2^(x - m), l = sum p, o = sum p v.  m moves only when a row's
@@ -245,7 +245,7 @@ __device__ void consume(const DecodeArgs& a, const BatchArgs& b, const Cursor& c
                     __syncwarp();
                     fence_proxy_async();   // before the next copy into this stage
                 }
-                float s[2][4] = {};
+                float s[2][4] = {}, odd[2][4] = {};   // two chains of products for each 8 keys (3% on short rows)
                 const int kr = warp * 16 + (lane & 7) + ((lane >> 4) << 3);   // key rows 0-7, then 8-15
                 const int kc = (lane >> 3) & 1;                               // low, high 8 of the k-step
 #pragma unroll
@@ -253,8 +253,13 @@ __device__ void consume(const DecodeArgs& a, const BatchArgs& b, const Cursor& c
                     uint32_t kf[4];
                     const int c = 2 * k + kc;
                     ldmatrix4(kf, swizzled(kbase + (c >> 3) * (kKeys * 128), kr, c & 7));
-                    mma16816<DT>(s[0], qf[k], kf[0], kf[1]);
-                    mma16816<DT>(s[1], qf[k], kf[2], kf[3]);
+                    mma16816<DT>(k & 1 ? odd[0] : s[0], qf[k], kf[0], kf[1]);
+                    mma16816<DT>(k & 1 ? odd[1] : s[1], qf[k], kf[2], kf[3]);
+                }
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    s[0][e] += odd[0][e];
+                    s[1][e] += odd[1][e];
                 }
                 const bool masked = key0 + 16 > all_hi || key0 < all_lo;
                 float mx[2] = {-INFINITY, -INFINITY};
