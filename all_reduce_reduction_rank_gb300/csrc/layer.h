@@ -40,6 +40,8 @@ struct BatchArgs {
 
 inline BatchArgs batch_args(const KvCache& kv, const ar_batch_t& b, int window)
 {
+    // positions lie within 2^30 of 0 on both sides: a window of 2^30 is none, and differences fit 32 bits
+    if (window > 1 << 30) window = 1 << 30;
     int shift = 4;
     while ((1 << shift) < kv.d.page_size) ++shift;
     return BatchArgs{b.q_start, b.kv_len, b.page_table, b.table_stride, (int)b.tokens, b.seqs, shift,

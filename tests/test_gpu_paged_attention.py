@@ -103,6 +103,15 @@ def test_windows(window, new, kv):
     check(2, 1, 4, 128, 32, "bf16", new, kv, window=window, seed=window)
 
 
+@pytest.mark.parametrize("max_new", [1, 500])
+def test_the_widest_window_is_none(max_new):
+    # also for rows before the first key, whose lower end would pass 32 bits
+    new, kv = [9, 1], [4, 300]
+    with Layer(2, 1, 64, 16, "f16", new, kv, max_new=max_new) as L:
+        q, out = run(L, 3, window=2**31 - 1)
+        compare(L, q, out, 3, L.dim**-0.5, 0)
+
+
 @pytest.mark.parametrize("max_new", [1, 500])   # both kernels, whatever the batch is
 def test_rows_that_see_nothing_are_zero(max_new):
     new, kv = [3, 2, 5, 1, 40], [1, 0, 5, 0, 7]
