@@ -1,24 +1,26 @@
 // Paged attention for few query rows per kv head: decode steps of one token
 // a sequence, or of a few drafted ones.
 //
-// A row tile holds at most 16 rows (new tokens x the query heads that share a
-// kv head), and every key and value of the sequence is read for it once, so
-// the bound is HBM: 4 D bytes per key and head against 64 D flops on the tile,
+// A row tile holds at most 8 or 16 rows (new tokens x the query heads that share
+// a kv head), and every key and value of the sequence is read for it once, so
+// the bound is HBM: 4 D bytes per key and head against 64 D flops on a tile of 16,
 // 16 flops per byte where the machine's tensor cores could do 280.  The
-// products therefore use mma.sync m16n8k16, whose 16 rows waste least, and the
-// design is about keeping enough copies in flight: one warp issues tensor
+// products therefore use mma.sync m16n8k16, whose tiles waste least: S = Q K^T
+// with 16 rows, and with 8 the transposed products S^T = K Q^T, O^T = V^T P^T,
+// half as many (8 sequences of 700 keys, 8 heads a kv head: 12.2 us with 16 rows,
+// 10.5 with 8).  The design is about keeping enough copies in flight: one warp issues tensor
 // copies of 64-key tiles (K and V) into a ring of stages, two CTAs of an SM
 // together holding about 190 KB of them, and four warps each take 16 keys of
 // every tile with their own running maximum, sum and output accumulators, so
 // nothing but the ring's barriers is shared until a row tile's keys end.
 //
 // Measured on GB300 (n = 8 bf16, heads of 128, 8 query heads a kv head): 64
-// sequences of 1 to 8192 keys, 792 MB: 130 us, 6.1 TB/s (91% of the copy rate); 4
+// sequences of 1 to 8192 keys, 792 MB: 127 us, 6.25 TB/s (93% of the copy rate); 4
 // sequences of 70 to 131 thousand keys (n = 4 fp16, 1.77 GB): 266 us, 6.65 TB/s
-// (100%); one sequence of 1500 keys: 9.7 us, where launch, split, page, copy, two
+// (100%); one sequence of 1500 keys: 8.7 us, where launch, split, page, copy, two
 // tiles and the join follow one another.  Short sequences are bound by the same
-// chain per row tile, about 3.5 us (64 sequences of 300 keys: 28 us for 12.5 us of
-// bytes); the tensor pipe is 17% busy, the warps wait for one another's results.
+// chain per row tile (64 sequences of 300 keys: 25 us for 12.5 us of bytes); the
+// tensor pipe is 17% busy with 16 rows, the warps wait for one another's results.
 //
 // Softmax in one pass, base 2: with x = scale log2(e) (q . k), a running
 // reference m, p = 2^(x - m), l = sum p, o = sum p v.  m moves only when a row's
@@ -37,8 +39,6 @@ namespace {
 constexpr int kKeys = 64;                    // keys of a tile
 constexpr int kWarps = 4;                    // consumers, 16 keys each
 constexpr int kTh = 32 * (kWarps + 1);
-constexpr int kRows = 16;
-constexpr int kCtas = 2;                     // per SM
 constexpr float kSlack = 8.0f;               // log2 of how far p may pass 1
 
 // a row tile's start and end weigh a key tile more (0 / 1 / 2 / 3: 8 sequences of 700
@@ -46,20 +46,25 @@ constexpr float kSlack = 8.0f;               // log2 of how far p may pass 1
 using DecodeSplit = Split<kKeys, 1, 4>;
 
 template <int D> constexpr int kTileBytes = kKeys * D * 2;
-template <int D> constexpr int kStages = D == 128 ? 3 : 6;
-template <int D> constexpr int kPartFloats = kRows * (D + 2);
+// per SM.  With 8 rows three CTAs of two stages fit as well: 16.5 for 13.9 us at one sequence of
+// 8000 keys (n = 2, 4 kv heads), 27.0 for 25.1 at 64 of 300, 124.5 for 127 at 64 of 1 to 8192.
+constexpr int kCtas = 2;
+template <int D> constexpr int kStages = 3 * (128 / D);
+template <int ROWS, int D> constexpr int kAccStride = ROWS == 8 ? D + 4 : D;   // floats; + 4: no bank conflicts
+template <int ROWS, int D> constexpr int kPartFloats = ROWS * (D + 2);
 
 struct DecodeShared {
     uint64_t full[6], empty[6];
-    float m[kWarps][kRows], l[kWarps][kRows];
-    float top[kRows], sum[kRows];
+    float m[kWarps][16], l[kWarps][16];
+    float top[16], sum[16];
     SplitShared split;
     int gave_up, last;
 };
-static_assert(sizeof(DecodeShared) <= 1024, "the shared memory of two CTAs fits one SM exactly");
+static_assert(sizeof(DecodeShared) <= 1024, "the shared memory of an SM's CTAs fits it exactly");
 
 // stages, then two accumulator buffers, then DecodeShared
-template <int D> constexpr int kSmem = kStages<D> * 2 * kTileBytes<D> + 2 * kRows * D * 4 + 1024;
+template <int ROWS, int D>
+constexpr int kSmem = kStages<D> * 2 * kTileBytes<D> + 2 * ROWS * kAccStride<ROWS, D> * 4 + 1024;
 
 struct DecodeArgs {
     const void* q[kMaxRanks];
@@ -106,6 +111,14 @@ __device__ __forceinline__ void ldmatrix4_trans(uint32_t* r, uint32_t addr)
                  : "memory");
 }
 
+// Transposes an 8 x 8 matrix of 16-bit elements, two of a row a thread.
+__device__ __forceinline__ uint32_t transpose8(uint32_t x)
+{
+    uint32_t y;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
+}
+
 __device__ __forceinline__ void consumers_sync() { asm volatile("bar.sync 1, %0;" ::"n"(32 * kWarps) : "memory"); }
 
 // A segment's rows: rank, kv head, first query head and number of heads, first
@@ -128,8 +141,8 @@ __device__ __forceinline__ RowTile row_tile(const DecodeArgs& a, const Segment& 
 }
 
 template <int D>
-__device__ void produce(const DecodeArgs& a, const BatchArgs& b, const Cursor& cur, const Seq& at, uint8_t* stages, DecodeShared* sh,
-                        DevStatus* st)
+__device__ void produce(const DecodeArgs& a, const BatchArgs& b, const Cursor& cur, const Seq& at, uint8_t* stages,
+                        DecodeShared* sh, DevStatus* st)
 {
     const int lane = threadIdx.x & 31;
     const int per_page = kKeys / a.box_tokens;         // boxes of a tile along the keys: 1, 2 or 4
@@ -184,15 +197,19 @@ __device__ void produce(const DecodeArgs& a, const BatchArgs& b, const Cursor& c
         }
 }
 
-template <int DT, int D>
+template <int DT, int D, int ROWS>
 __device__ void consume(const DecodeArgs& a, const BatchArgs& b, const Cursor& cur, const Seq& at, uint8_t* stages, float* acc,
                         DecodeShared* sh, DevStatus* st)
 {
     using T = typename Payload<DT>::scalar_t;
     constexpr int KS = D / 16;      // k-steps of q . k
-    constexpr int NT = D / 8;       // 8-wide column tiles of the output
+    constexpr int NT = ROWS == 8 ? D / 16 : D / 8;   // tiles of the output: 16 of D by 8 rows, or 16 rows by 8 of D
+    constexpr int AS = kAccStride<ROWS, D>;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int r0 = lane >> 2, col = (lane & 3) * 2;
+    // the two rows whose statistics this thread keeps, and the lanes it shares them with
+    auto row_of = [&](int i) { return ROWS == 8 ? col + i : r0 + 8 * i; };
+    constexpr int SHARED = ROWS == 8 ? 3 : 2, FIRST = ROWS == 8 ? 4 : 1;   // log2 of the lanes, first lane bit
     Walk<DecodeSplit> walk(cur, at);
     Segment seg;
     int stage = 0;
@@ -201,21 +218,25 @@ __device__ void consume(const DecodeArgs& a, const BatchArgs& b, const Cursor& c
     while (walk.next(b, a.tm, seg, st)) {
         const RowTile rt = row_tile(a, seg);
         const T* qp = static_cast<const T*>(a.q[rt.rank]) + (size_t)rt.head0 * D;
-        // rows of this thread: r0 and r0 + 8
         int limit[2], lower[2];
-        uint32_t qf[KS][4];
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
+            const int r = row_of(i);
+            limit[i] = r < rt.rows ? seg.q.c0 + rt.tok0 + r / rt.heads + 1 : 0;
+            lower[i] = b.window > 0 ? limit[i] - b.window : 0;
+        }
+        // q, the fragments of rows r0 (and r0 + 8)
+        uint32_t qf[KS][ROWS / 4];
+#pragma unroll
+        for (int i = 0; i < ROWS / 8; ++i) {
             const int r = r0 + 8 * i;
             const bool there = r < rt.rows;
             const int tok = rt.tok0 + r / rt.heads, hd = r % rt.heads;
-            limit[i] = there ? seg.q.c0 + tok + 1 : 0;
-            lower[i] = b.window > 0 ? limit[i] - b.window : 0;
             const T* row = qp + (size_t)(seg.q.q0 + tok) * a.q_stride + (size_t)hd * D + col;
 #pragma unroll
             for (int k = 0; k < KS; ++k) {
                 qf[k][i] = there ? *reinterpret_cast<const uint32_t*>(row + 16 * k) : 0u;
-                qf[k][2 + i] = there ? *reinterpret_cast<const uint32_t*>(row + 16 * k + 8) : 0u;
+                qf[k][ROWS / 8 + i] = there ? *reinterpret_cast<const uint32_t*>(row + 16 * k + 8) : 0u;
             }
         }
         // keys that every row of the tile sees
@@ -245,41 +266,48 @@ __device__ void consume(const DecodeArgs& a, const BatchArgs& b, const Cursor& c
                     __syncwarp();
                     fence_proxy_async();   // before the next copy into this stage
                 }
-                float s[2][4] = {}, odd[2][4] = {};   // two chains of products for each 8 keys (3% on short rows)
-                const int kr = warp * 16 + (lane & 7) + ((lane >> 4) << 3);   // key rows 0-7, then 8-15
-                const int kc = (lane >> 3) & 1;                               // low, high 8 of the k-step
+                // scores of 16 keys: S^T (16 keys by 8 rows), or S (16 rows by two times 8 keys); element e
+                // of s[nt] is row_of(ROW(e)) and key KEY(nt, e).  Two chains of products for each
+                // (3% on short rows).
+                constexpr int NS = ROWS / 8;
+                auto row_i = [](int e) { return ROWS == 8 ? e & 1 : e >> 1; };
+                auto key_of = [&](int nt, int e) { return ROWS == 8 ? r0 + 8 * (e >> 1) : 8 * nt + col + (e & 1); };
+                float s[NS][4] = {}, odd[NS][4] = {};
+                const int hi8 = (lane >> 4) << 3, mid8 = (lane >> 3) & 1;
+                const int kr = warp * 16 + (lane & 7) + (ROWS == 8 ? mid8 * 8 : hi8);
+                const int kc = ROWS == 8 ? lane >> 4 : mid8;                  // low, high 8 of the k-step
 #pragma unroll
                 for (int k = 0; k < KS; ++k) {
                     uint32_t kf[4];
                     const int c = 2 * k + kc;
                     ldmatrix4(kf, swizzled(kbase + (c >> 3) * (kKeys * 128), kr, c & 7));
-                    mma16816<DT>(k & 1 ? odd[0] : s[0], qf[k], kf[0], kf[1]);
-                    mma16816<DT>(k & 1 ? odd[1] : s[1], qf[k], kf[2], kf[3]);
-                }
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    s[0][e] += odd[0][e];
-                    s[1][e] += odd[1][e];
+                    if constexpr (ROWS == 8) {
+                        mma16816<DT>(k & 1 ? odd[0] : s[0], kf, qf[k][0], qf[k][1]);
+                    } else {
+                        mma16816<DT>(k & 1 ? odd[0] : s[0], qf[k], kf[0], kf[1]);
+                        mma16816<DT>(k & 1 ? odd[1] : s[1], qf[k], kf[2], kf[3]);
+                    }
                 }
                 const bool masked = key0 + 16 > all_hi || key0 < all_lo;
                 float mx[2] = {-INFINITY, -INFINITY};
 #pragma unroll
-                for (int nt = 0; nt < 2; ++nt)
+                for (int nt = 0; nt < NS; ++nt)
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        float x = s[nt][e] * a.scale_log2;
+                        float x = (s[nt][e] + odd[nt][e]) * a.scale_log2;
+                        const int i = row_i(e);
                         if (masked) {
-                            const int key = key0 + 8 * nt + col + (e & 1);
-                            if (key >= limit[e >> 1] || key < lower[e >> 1]) x = -INFINITY;
+                            const int key = key0 + key_of(nt, e);
+                            if (key >= limit[i] || key < lower[i]) x = -INFINITY;
                         }
                         s[nt][e] = x;
-                        mx[e >> 1] = fmaxf(mx[e >> 1], x);
+                        mx[i] = fmaxf(mx[i], x);
                     }
                 bool move = false;
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
-                    mx[i] = fmaxf(mx[i], __shfl_xor_sync(0xffffffffu, mx[i], 1));
-                    mx[i] = fmaxf(mx[i], __shfl_xor_sync(0xffffffffu, mx[i], 2));
+#pragma unroll
+                    for (int w = 0; w < SHARED; ++w) mx[i] = fmaxf(mx[i], __shfl_xor_sync(0xffffffffu, mx[i], FIRST << w));
                     move |= mx[i] > m[i] + kSlack;
                 }
                 if (__any_sync(0xffffffffu, move)) {
@@ -292,37 +320,46 @@ __device__ void consume(const DecodeArgs& a, const BatchArgs& b, const Cursor& c
                         l[i] *= f[i];
                     }
 #pragma unroll
-                    for (int n = 0; n < NT; ++n) {
-                        o[n][0] *= f[0];
-                        o[n][1] *= f[0];
-                        o[n][2] *= f[1];
-                        o[n][3] *= f[1];
-                    }
-                }
-                uint32_t pf[4];
-                float p[2][4];
+                    for (int n = 0; n < NT; ++n)
 #pragma unroll
-                for (int nt = 0; nt < 2; ++nt)
+                        for (int e = 0; e < 4; ++e) o[n][e] *= f[row_i(e)];
+                }
+                float p[NS][4];
+#pragma unroll
+                for (int nt = 0; nt < NS; ++nt)
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        const float ref = m[e >> 1] == -INFINITY ? 0.0f : m[e >> 1];
+                        const int i = row_i(e);
+                        const float ref = m[i] == -INFINITY ? 0.0f : m[i];
                         p[nt][e] = ex2(s[nt][e] - ref);
-                        l[e >> 1] += p[nt][e];
+                        l[i] += p[nt][e];
                     }
                 // rounded to the cache's type: the product's operand (at most half a step of it each)
-                pf[0] = Payload<DT>::narrow(&p[0][0]);
-                pf[1] = Payload<DT>::narrow(&p[0][2]);
-                pf[2] = Payload<DT>::narrow(&p[1][0]);
-                pf[3] = Payload<DT>::narrow(&p[1][2]);
-                const int vr = warp * 16 + (lane & 15);     // keys 0-7, 8-15
-                const int vc = lane >> 4;                   // columns 0-7, 8-15
+                if constexpr (ROWS == 8) {
+                    // O^T += V^T P^T: the scores' place holds P^T by rows, the operand wants it by columns
+                    const uint32_t p0 = transpose8(Payload<DT>::narrow(&p[0][0]));
+                    const uint32_t p1 = transpose8(Payload<DT>::narrow(&p[0][2]));
+                    const int vr = warp * 16 + (lane & 7) + hi8;    // keys 0-7, 8-15
 #pragma unroll
-                for (int n = 0; n < NT; n += 2) {
-                    uint32_t vf[4];
-                    const int c = n + vc;
-                    ldmatrix4_trans(vf, swizzled(vbase + (c >> 3) * (kKeys * 128), vr, c & 7));
-                    mma16816<DT>(o[n], pf, vf[0], vf[1]);
-                    mma16816<DT>(o[n + 1], pf, vf[2], vf[3]);
+                    for (int n = 0; n < NT; ++n) {
+                        uint32_t vf[4];
+                        const int c = 2 * n + mid8;                 // low, high 8 of the 16 columns
+                        ldmatrix4_trans(vf, swizzled(vbase + (c >> 3) * (kKeys * 128), vr, c & 7));
+                        mma16816<DT>(o[n], vf, p0, p1);
+                    }
+                } else {
+                    const uint32_t pf[4] = {Payload<DT>::narrow(&p[0][0]), Payload<DT>::narrow(&p[0][2]),
+                                            Payload<DT>::narrow(&p[NS - 1][0]), Payload<DT>::narrow(&p[NS - 1][2])};
+                    const int vr = warp * 16 + (lane & 15);         // keys 0-7, 8-15
+                    const int vc = lane >> 4;                       // columns 0-7, 8-15
+#pragma unroll
+                    for (int n = 0; n < NT; n += 2) {
+                        uint32_t vf[4];
+                        const int c = n + vc;
+                        ldmatrix4_trans(vf, swizzled(vbase + (c >> 3) * (kKeys * 128), vr, c & 7));
+                        mma16816<DT>(o[n], pf, vf[0], vf[1]);
+                        mma16816<DT>(o[n + 1], pf, vf[2], vf[3]);
+                    }
                 }
             }
             __syncwarp();
@@ -336,18 +373,18 @@ __device__ void consume(const DecodeArgs& a, const BatchArgs& b, const Cursor& c
         // join the four warps: maxima and sums, then the accumulators, warps 0 and 2 first
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-            l[i] += __shfl_xor_sync(0xffffffffu, l[i], 1);
-            l[i] += __shfl_xor_sync(0xffffffffu, l[i], 2);
-            if ((lane & 3) == 0) {
-                sh->m[warp][r0 + 8 * i] = m[i];
-                sh->l[warp][r0 + 8 * i] = l[i];
+#pragma unroll
+            for (int w = 0; w < SHARED; ++w) l[i] += __shfl_xor_sync(0xffffffffu, l[i], FIRST << w);
+            if ((lane & (((1 << SHARED) - 1) * FIRST)) == 0) {
+                sh->m[warp][row_of(i)] = m[i];
+                sh->l[warp][row_of(i)] = l[i];
             }
         }
         consumers_sync();
         float f[2];
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-            const int r = r0 + 8 * i;
+            const int r = row_of(i);
             float top = -INFINITY, sum = 0.0f;
 #pragma unroll
             for (int w = 0; w < kWarps; ++w) top = fmaxf(top, sh->m[w][r]);
@@ -355,27 +392,36 @@ __device__ void consume(const DecodeArgs& a, const BatchArgs& b, const Cursor& c
             for (int w = 0; w < kWarps; ++w)
                 sum += sh->m[w][r] == -INFINITY ? 0.0f : sh->l[w][r] * ex2(sh->m[w][r] - top);
             f[i] = m[i] == -INFINITY ? 0.0f : ex2(m[i] - top);
-            if (warp == 0 && (lane & 3) == 0) {   // the barriers of the turns below publish them
+            if (warp == 0 && (lane & (((1 << SHARED) - 1) * FIRST)) == 0) {   // the barriers of the turns below publish them
                 sh->top[r] = top;
                 sh->sum[r] = sum;
             }
         }
-        float* mine = acc + (warp >> 1) * (kRows * D);
+        float* mine = acc + (warp >> 1) * (ROWS * AS);
 #pragma unroll
         for (int turn = 0; turn < 2; ++turn) {
             if ((warp & 1) == turn) {
 #pragma unroll
                 for (int n = 0; n < NT; ++n)
+                    if constexpr (ROWS == 8) {
 #pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        float2* at = reinterpret_cast<float2*>(mine + (r0 + 8 * i) * D + 8 * n + col);
-                        float2 x = make_float2(o[n][2 * i] * f[i], o[n][2 * i + 1] * f[i]);
-                        if (turn == 1) {
-                            const float2 y = *at;
-                            x.x += y.x;
-                            x.y += y.y;
+                        for (int e = 0; e < 4; ++e) {
+                            float* at = mine + (col + (e & 1)) * AS + 16 * n + r0 + 8 * (e >> 1);
+                            const float x = o[n][e] * f[e & 1];
+                            *at = turn == 1 ? x + *at : x;
                         }
-                        *at = x;
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            float2* at = reinterpret_cast<float2*>(mine + (r0 + 8 * i) * AS + 8 * n + col);
+                            float2 x = make_float2(o[n][2 * i] * f[i], o[n][2 * i + 1] * f[i]);
+                            if (turn == 1) {
+                                const float2 y = *at;
+                                x.x += y.x;
+                                x.y += y.y;
+                            }
+                            *at = x;
+                        }
                     }
             }
             consumers_sync();
@@ -387,11 +433,11 @@ __device__ void consume(const DecodeArgs& a, const BatchArgs& b, const Cursor& c
             uint2 w = make_uint2(Payload<DT>::narrow(v), Payload<DT>::narrow(v + 2));
             *reinterpret_cast<uint2*>(op + (size_t)(seg.q.q0 + tok) * a.out_stride + (size_t)hd * D + d) = w;
         };
-        float* part = a.partial + (size_t)seg.slot * kPartFloats<D>;
+        float* part = a.partial + (size_t)seg.slot * kPartFloats<ROWS, D>;
         for (int i = tid; i < rt.rows * (D / 4); i += 32 * kWarps) {
             const int r = i / (D / 4), d = i % (D / 4) * 4;
-            const float4 x = *reinterpret_cast<const float4*>(acc + r * D + d);
-            const float4 y = *reinterpret_cast<const float4*>(acc + kRows * D + r * D + d);
+            const float4 x = *reinterpret_cast<const float4*>(acc + r * AS + d);
+            const float4 y = *reinterpret_cast<const float4*>(acc + ROWS * AS + r * AS + d);
             float4 z = make_float4(x.x + y.x, x.y + y.y, x.z + y.z, x.w + y.w);
             const float top = sh->top[r], sum = sh->sum[r];
             if (seg.parts == 1) {
@@ -400,8 +446,8 @@ __device__ void consume(const DecodeArgs& a, const BatchArgs& b, const Cursor& c
             } else {
                 __stcg(reinterpret_cast<float4*>(part + r * D + d), z);
                 if (d == 0) {
-                    __stcg(part + kRows * D + r, top);
-                    __stcg(part + kRows * D + kRows + r, sum);
+                    __stcg(part + ROWS * D + r, top);
+                    __stcg(part + ROWS * D + ROWS + r, sum);
                 }
             }
         }
@@ -431,9 +477,9 @@ __device__ void consume(const DecodeArgs& a, const BatchArgs& b, const Cursor& c
 #pragma unroll
                         for (int k = 0; k < 8; ++k) {
                             const float* from =
-                                a.partial + (size_t)part_slot(seg.first_cta, min(k0 + k, seg.parts - 1)) * kPartFloats<D>;
-                            m[k] = k0 + k < seg.parts ? __ldcg(from + kRows * D + r) : -INFINITY;
-                            l[k] = __ldcg(from + kRows * D + kRows + r);
+                                a.partial + (size_t)part_slot(seg.first_cta, min(k0 + k, seg.parts - 1)) * kPartFloats<ROWS, D>;
+                            m[k] = k0 + k < seg.parts ? __ldcg(from + ROWS * D + r) : -INFINITY;
+                            l[k] = __ldcg(from + ROWS * D + ROWS + r);
                             x[k] = __ldcg(reinterpret_cast<const float4*>(from + r * D + d));
                         }
                         float to = top;
@@ -462,15 +508,16 @@ __device__ void consume(const DecodeArgs& a, const BatchArgs& b, const Cursor& c
     }
 }
 
-template <int DT, int D>
+template <int DT, int D, int ROWS>
 __global__ void __launch_bounds__(kTh, kCtas)
 attention_decode_kernel(const __grid_constant__ DecodeArgs a, const BatchArgs b, DevStatus* st)
 {
     extern __shared__ __align__(1024) uint8_t smem[];
-    float* acc = reinterpret_cast<float*>(smem + kStages<D> * 2 * kTileBytes<D>);
-    DecodeShared* sh = reinterpret_cast<DecodeShared*>(acc + 2 * kRows * D);
+    constexpr int STAGES = kStages<D>;
+    float* acc = reinterpret_cast<float*>(smem + STAGES * 2 * kTileBytes<D>);
+    DecodeShared* sh = reinterpret_cast<DecodeShared*>(acc + 2 * ROWS * kAccStride<ROWS, D>);
     if (threadIdx.x == 0) {
-        for (int i = 0; i < kStages<D>; ++i) {
+        for (int i = 0; i < STAGES; ++i) {
             mbar_init(&sh->full[i], 1);
             mbar_init(&sh->empty[i], kWarps);
         }
@@ -493,7 +540,7 @@ attention_decode_kernel(const __grid_constant__ DecodeArgs a, const BatchArgs b,
     if (threadIdx.x >= 32 * kWarps)
         produce<D>(a, b, cur, at, smem, sh, st);
     else
-        consume<DT, D>(a, b, cur, at, smem, acc, sh, st);
+        consume<DT, D, ROWS>(a, b, cur, at, smem, acc, sh, st);
     pdl_release();
 }
 
@@ -501,7 +548,7 @@ attention_decode_kernel(const __grid_constant__ DecodeArgs a, const BatchArgs b,
 
 size_t attention_decode_partial_floats(const Handle& h, int head_dim)
 {
-    return (size_t)(2 * kCtas * h.sm_count) * (size_t)(kRows * (head_dim + 2));
+    return (size_t)(2 * kCtas * h.sm_count) * (size_t)(16 * (head_dim + 2));
 }
 
 size_t attention_decode_counters(const Handle& h) { return (size_t)(kCtas * h.sm_count); }
@@ -523,33 +570,40 @@ int launch_attention_decode(KvCache& kv, const ar_batch_t& b, const AttnCall& c,
     a.n = h.n;
     a.kv_heads = kv.d.kv_heads;
     a.group = c.q_heads / kv.d.kv_heads;
-    a.tile_heads = a.group < kRows ? a.group : kRows;
+    // rows of a sequence per head group: 8 if they all fit
+    const bool eight = (size_t)b.max_new * (size_t)a.group <= 8;
+    const int rows = eight ? 8 : 16;
+    a.tile_heads = a.group < rows ? a.group : rows;
     a.head_groups = (a.group + a.tile_heads - 1) / a.tile_heads;
-    a.tm = kRows / a.tile_heads;
+    a.tm = rows / a.tile_heads;
     a.box_tokens = kv.box_tokens;
     a.min_units = 2;
     a.few = b.seqs <= 256 && (b.max_new + a.tm - 1) / a.tm <= 8;
     const uint64_t moved = (uint64_t)h.n * b.tokens * c.q_heads * kv.d.head_dim * 2u * 2u;
-    auto run = [&](auto dtc, auto dc) -> int {
-        constexpr int DT = decltype(dtc)::value, D = decltype(dc)::value;
+    auto run = [&](auto dtc, auto dc, auto rc) -> int {
+        constexpr int DT = decltype(dtc)::value, D = decltype(dc)::value, ROWS = decltype(rc)::value;
         static std::atomic<uint32_t> attr_done{0};
         if (!once_per_device(attr_done, [&] {
-                return cudaFuncSetAttribute(attention_decode_kernel<DT, D>,
-                                            cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem<D>) == cudaSuccess;
+                return cudaFuncSetAttribute(attention_decode_kernel<DT, D, ROWS>,
+                                            cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem<ROWS, D>) == cudaSuccess;
             }))
             return AR_ERR_CUDA;
         rec_begin(h, s);
-        const cudaError_t e = launch_kernel(h, attention_decode_kernel<DT, D>, dim3((unsigned)(kCtas * h.sm_count)),
-                                            dim3(kTh), kSmem<D>, s, a, batch_args(kv, b, window), h.status);
+        const cudaError_t e =
+            launch_kernel(h, attention_decode_kernel<DT, D, ROWS>, dim3((unsigned)(kCtas * h.sm_count)), dim3(kTh),
+                          kSmem<ROWS, D>, s, a, batch_args(kv, b, window), h.status);
         rec_end(h, s, AR_K_ATTENTION_DECODE, moved);
         return e == cudaSuccess ? launch_status() : AR_ERR_CUDA;
+    };
+    auto sized = [&](auto dtc, auto dc) -> int {
+        return eight ? run(dtc, dc, std::integral_constant<int, 8>{}) : run(dtc, dc, std::integral_constant<int, 16>{});
     };
     using BF = std::integral_constant<int, AR_BF16>;
     using HF = std::integral_constant<int, AR_F16>;
     using D64 = std::integral_constant<int, 64>;
     using D128 = std::integral_constant<int, 128>;
-    if (kv.d.dtype == AR_BF16) return kv.d.head_dim == 128 ? run(BF{}, D128{}) : run(BF{}, D64{});
-    return kv.d.head_dim == 128 ? run(HF{}, D128{}) : run(HF{}, D64{});
+    if (kv.d.dtype == AR_BF16) return kv.d.head_dim == 128 ? sized(BF{}, D128{}) : sized(BF{}, D64{});
+    return kv.d.head_dim == 128 ? sized(HF{}, D128{}) : sized(HF{}, D64{});
 }
 
 }  // namespace argb
