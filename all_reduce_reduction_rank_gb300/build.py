@@ -20,8 +20,10 @@ OUT_DIR = PKG / "_build"
 LIB = PKG / "libar_gb300.so"
 SOURCES = ["api.cu", "one_shot.cu", "two_shot.cu", "ring.cu", "ll.cu", "ring_noalloc.cu", "rmsnorm.cu",
            "one_shot_modes.cu", "tree.cu", "ring_persistent.cu", "ring_cluster.cu", "ring_fused.cu",
-           "block_norm_f32.cu", "block_norm_bf16.cu", "block_norm_f16.cu", "rope_append.cu", "attention_decode.cu", "attention_chunk.cu", "layer_api.cu"]
-HEADERS = ["common.cuh", "internal.h", "bulk.cuh", "lines.cuh", "cluster.cuh", "block_norm.cuh", "layer.h", "paged.cuh", "tmem.cuh"]
+           "block_norm_f32.cu", "block_norm_bf16.cu", "block_norm_f16.cu", "rope_append.cu", "attention_decode.cu",
+           "attention_chunk.cu", "layer_api.cu"]
+HEADERS = ["common.cuh", "internal.h", "bulk.cuh", "lines.cuh", "cluster.cuh", "block_norm.cuh", "layer.h",
+           "paged.cuh", "tmem.cuh"]
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = [
