@@ -334,22 +334,36 @@ __device__ void consume(const DecodeArgs& a, const BatchArgs& b, const Cursor& c
                         p[nt][e] = ex2(s[nt][e] - ref);
                         l[i] += p[nt][e];
                     }
-                // rounded to the cache's type: the product's operand (at most half a step of it each)
+                // The product's operand has the cache's type: p = high + low, both rounded to it, so that
+                // what is lost is a half step of a half step.  Rounded once, the outputs of short batches
+                // were off by 1.4 times their own rounding; the second product is hidden behind the copies.
+                uint32_t high[2 * NS], low[2 * NS];
+#pragma unroll
+                for (int nt = 0; nt < NS; ++nt)
+#pragma unroll
+                    for (int e = 0; e < 4; e += 2) {
+                        float back[2];
+                        const uint32_t w = Payload<DT>::narrow(&p[nt][e]);
+                        Payload<DT>::widen(w, back);
+                        back[0] = p[nt][e] - back[0];
+                        back[1] = p[nt][e + 1] - back[1];
+                        high[2 * nt + e / 2] = w;
+                        low[2 * nt + e / 2] = Payload<DT>::narrow(back);
+                    }
                 if constexpr (ROWS == 8) {
                     // O^T += V^T P^T: the scores' place holds P^T by rows, the operand wants it by columns
-                    const uint32_t p0 = transpose8(Payload<DT>::narrow(&p[0][0]));
-                    const uint32_t p1 = transpose8(Payload<DT>::narrow(&p[0][2]));
+                    const uint32_t h0 = transpose8(high[0]), h1 = transpose8(high[1]);
+                    const uint32_t l0 = transpose8(low[0]), l1 = transpose8(low[1]);
                     const int vr = warp * 16 + (lane & 7) + hi8;    // keys 0-7, 8-15
 #pragma unroll
                     for (int n = 0; n < NT; ++n) {
                         uint32_t vf[4];
                         const int c = 2 * n + mid8;                 // low, high 8 of the 16 columns
                         ldmatrix4_trans(vf, swizzled(vbase + (c >> 3) * (kKeys * 128), vr, c & 7));
-                        mma16816<DT>(o[n], vf, p0, p1);
+                        mma16816<DT>(o[n], vf, h0, h1);
+                        mma16816<DT>(o[n], vf, l0, l1);
                     }
                 } else {
-                    const uint32_t pf[4] = {Payload<DT>::narrow(&p[0][0]), Payload<DT>::narrow(&p[0][2]),
-                                            Payload<DT>::narrow(&p[NS - 1][0]), Payload<DT>::narrow(&p[NS - 1][2])};
                     const int vr = warp * 16 + (lane & 15);         // keys 0-7, 8-15
                     const int vc = lane >> 4;                       // columns 0-7, 8-15
 #pragma unroll
@@ -357,8 +371,10 @@ __device__ void consume(const DecodeArgs& a, const BatchArgs& b, const Cursor& c
                         uint32_t vf[4];
                         const int c = n + vc;
                         ldmatrix4_trans(vf, swizzled(vbase + (c >> 3) * (kKeys * 128), vr, c & 7));
-                        mma16816<DT>(o[n], pf, vf[0], vf[1]);
-                        mma16816<DT>(o[n + 1], pf, vf[2], vf[3]);
+                        mma16816<DT>(o[n], high, vf[0], vf[1]);
+                        mma16816<DT>(o[n + 1], high, vf[2], vf[3]);
+                        mma16816<DT>(o[n], low, vf[0], vf[1]);
+                        mma16816<DT>(o[n + 1], low, vf[2], vf[3]);
                     }
                 }
             }

@@ -576,8 +576,9 @@ int ar_rope_append(ar_kv kv, const ar_batch_t* batch, const void* const* q, cons
  * the new tokens (ar_rope_append); cache slots at or past kv_len, and before
  * the window of a sequence's first new token, may hold anything, NaN included.
  * A non-finite value within them may reach every row of the sequence.
- * Scores, softmax statistics and sums are fp32; the probabilities are rounded
- * to the cache's type before they meet the values, the output once at the end.
+ * Scores, softmax statistics and sums are fp32; the probabilities meet the
+ * values in the cache's type, rounded to it once for chunks and as a sum of two
+ * such parts for few rows per kv head; the output is rounded once at the end.
  * Few rows per kv head (max_new x q_heads / kv_heads up to 16, 32 for heads of
  * 64) and more take different kernels; either is right for every batch, and the
  * result does not depend on how the keys are split over the CTAs in between (the
