@@ -8,7 +8,7 @@
 // products therefore use mma.sync m16n8k16, whose tiles waste least: S = Q K^T
 // with 16 rows, and with 8 the transposed products S^T = K Q^T, O^T = V^T P^T,
 // half as many (8 sequences of 700 keys, 8 heads a kv head: 12.2 us with 16 rows,
-// 10.5 with 8).  The design is about keeping enough copies in flight: one warp issues tensor
+// 10.6 with 8).  The design is about keeping enough copies in flight: one warp issues tensor
 // copies of 64-key tiles (K and V) into a ring of stages, two CTAs of an SM
 // together holding about 190 KB of them, and four warps each take 16 keys of
 // every tile with their own running maximum, sum and output accumulators, so
@@ -16,8 +16,8 @@
 //
 // Measured on GB300 (n = 8 bf16, heads of 128, 8 query heads a kv head): 64
 // sequences of 1 to 8192 keys, 792 MB: 127 us, 6.25 TB/s (93% of the copy rate); 4
-// sequences of 70 to 131 thousand keys (n = 4 fp16, 1.77 GB): 266 us, 6.65 TB/s
-// (100%); one sequence of 1500 keys: 8.7 us, where launch, split, page, copy, two
+// sequences of 70 to 131 thousand keys (n = 4 fp16, 1.77 GB): 258 us, 6.86 TB/s
+// (103%); one sequence of 1500 keys: 8.5 to 9.1 us, where launch, split, page, copy, two
 // tiles and the join follow one another.  Short sequences are bound by the same
 // chain per row tile (64 sequences of 300 keys: 25 us for 12.5 us of bytes); the
 // tensor pipe is 17% busy with 16 rows, the warps wait for one another's results.
