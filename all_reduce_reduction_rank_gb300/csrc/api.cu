@@ -899,7 +899,7 @@ int ar_status_info(ar_handle hd, ar_status_info_t* info)
     });
     if (info) {
         info->code = rc != AR_OK ? rc : st.code;
-        info->rank = st.code ? st.rank : -1;
+        info->rank = st.code == AR_ERR_FLAG_TIMEOUT ? st.rank : -1;   // no other error belongs to a rank's line
         info->line = st.line;
         info->lines_skipped = st.skipped;
     }
