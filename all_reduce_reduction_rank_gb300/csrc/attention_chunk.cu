@@ -157,6 +157,7 @@ __device__ void produce(const ChunkArgs& a, const BatchArgs& b, uint8_t* stages,
     while (ok && next_segment(b, 2 * a.half_tokens, sh, st)) {
         const int tiles = max(half_tile(a, seg, 0).tiles, half_tile(a, seg, 1).tiles);
         const int kv_head = seg.head % a.kv_heads, rank = seg.head / a.kv_heads;
+        if (rank == b.absent) break;
         const int32_t* row = b.table + (size_t)seg.s * b.table_stride;
         const int j0 = seg.j0, key_lo = seg.span.key_lo, key_hi = seg.span.key_hi;
         for (int j = j0; ok && j < j0 + tiles; ++j) {
@@ -188,13 +189,7 @@ __device__ void produce(const ChunkArgs& a, const BatchArgs& b, uint8_t* stages,
             }
         }
     }
-    // after a wait that ran out the copies in flight still land in this CTA's shared memory
-    if (!ok)
-        for (uint32_t k = 0; k < issued && k < (uint32_t)kStages<D>; ++k) {
-            stage = stage == 0 ? kStages<D> - 1 : stage - 1;
-            if (stage == kStages<D> - 1) phase ^= 1;
-            wait_a_second(&sh->full[stage], phase, nullptr);
-        }
+    wait_for_ring(sh->full, kStages<D>, issued, stage, phase, st);
 }
 
 // The halves' queries, as soon as the last product that reads the previous
@@ -206,20 +201,16 @@ __device__ void load_queries(const ChunkArgs& a, const BatchArgs& b, uint8_t* q_
 {
     const int lane = threadIdx.x & 31;
     const Segment& seg = sh->seg[threadIdx.x / 32];
-    uint32_t phase[2] = {0, 0};
-    bool first[2] = {true, true}, ok = true, in_flight[2] = {false, false};
+    uint32_t issued[2] = {0, 0};
+    bool ok = true;
     while (ok && next_segment(b, 2 * a.half_tokens, sh, st)) {
         const int kv_head = seg.head % a.kv_heads, rank = seg.head / a.kv_heads;
         for (int h = 0; ok && h < 2; ++h) {
             const HalfTile x = half_tile(a, seg, h);
             if (x.tiles == 0) continue;
-            if (!first[h]) {
-                warp_wait(ok, &sh->q_empty[h], phase[h], sh, st);
-                phase[h] ^= 1;
-                if (!ok) break;
-            }
-            first[h] = false;
-            in_flight[h] = true;
+            if (issued[h] > 0) warp_wait(ok, &sh->q_empty[h], (issued[h] - 1) & 1, sh, st);
+            if (!ok) break;
+            ++issued[h];
             if (lane == 0) {
                 mbar_arrive_expect_tx(&sh->q_full[h], (uint32_t)(a.half_tokens * a.group * D * 2));
                 for (int d = 0; d < D; d += 64)
@@ -229,10 +220,8 @@ __device__ void load_queries(const ChunkArgs& a, const BatchArgs& b, uint8_t* q_
             __syncwarp();
         }
     }
-    // after a wait that ran out: the last copies, whose phase is the one after the last q_empty
-    if (!ok)
-        for (int h = 0; h < 2; ++h)
-            if (in_flight[h]) wait_a_second(&sh->q_full[h], phase[h], nullptr);
+    for (int h = 0; h < 2; ++h)
+        if (issued[h] > 0) wait_for_own(&sh->q_full[h], (issued[h] - 1) & 1, st);
 }
 
 // The tiles that the products of key tile i read beside the probabilities, V of
@@ -284,7 +273,8 @@ __device__ void watch_tiles(const ChunkArgs& a, const BatchArgs& b, uint8_t* sta
                     // one phase at a time: not before the softmax warps' arrivals of the last
                     warp_wait(ok, &sh->p_full[h][0], p_phase[h] ^ 1, sh, st);
                     p_phase[h] ^= 1;
-                    if (lane == 0) mbar_arrive(&sh->p_full[h][0]);
+                    // (nothing after giving up: the products would read, and free, tiles that have not landed)
+                    if (ok && lane == 0) mbar_arrive(&sh->p_full[h][0]);
                 }
         }
     }
@@ -376,7 +366,7 @@ __device__ void issue(const ChunkArgs& a, const BatchArgs& b, uint8_t* q_tiles, 
     // nothing that was issued may still run when the tensor memory is freed
     if (elect_one()) mma_commit(&sh->drained);
     __syncwarp();
-    if (!wait_a_second(&sh->drained, 0, nullptr)) report_wait_timeout(st);
+    wait_for_own(&sh->drained, 0, st);
 }
 
 __device__ __forceinline__ uint64_t pack2(float x, float y)

@@ -158,6 +158,7 @@ __device__ void produce(const DecodeArgs& a, const BatchArgs& b, const Cursor& c
     bool ok = true;
     while (ok && walk.next(b, a.tm, seg, st)) {
         const RowTile rt = row_tile(a, seg);
+        if (rt.rank == b.absent) break;
         const CUtensorMap* map = a.maps + (is_v ? a.n : 0) + rt.rank;
         const int32_t* row = b.table + (size_t)seg.s * b.table_stride;
         for (int j = seg.j0; ok && j < seg.j1; ++j) {
@@ -188,13 +189,7 @@ __device__ void produce(const DecodeArgs& a, const BatchArgs& b, const Cursor& c
             }
         }
     }
-    // after a wait that ran out the copies in flight still land in this CTA's shared memory
-    if (!ok)
-        for (uint32_t k = 0; k < issued && k < (uint32_t)kStages<D>; ++k) {
-            stage = stage == 0 ? kStages<D> - 1 : stage - 1;
-            if (stage == kStages<D> - 1) phase ^= 1;
-            wait_a_second(&sh->full[stage], phase, nullptr);
-        }
+    wait_for_ring(sh->full, kStages<D>, issued, stage, phase, st);
 }
 
 template <int DT, int D, int ROWS>
@@ -379,7 +374,8 @@ __device__ void consume(const DecodeArgs& a, const BatchArgs& b, const Cursor& c
                 }
             }
             __syncwarp();
-            if (lane == 0) mbar_arrive(&sh->empty[stage]);
+            // (a warp that has given up frees nothing: the others may still read the tile)
+            if (ok && lane == 0) mbar_arrive(&sh->empty[stage]);
             if (++stage == kStages<D>) {
                 stage = 0;
                 phase ^= 1;

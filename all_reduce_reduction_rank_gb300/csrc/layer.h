@@ -36,6 +36,7 @@ struct BatchArgs {
     int page_shift;                  // log2(page_size)
     int pages;
     int window;                      // 0: none
+    int absent;                      // rank whose keys never arrive at the attention kernels (-1: none)
 };
 
 inline BatchArgs batch_args(const KvCache& kv, const ar_batch_t& b, int window)
@@ -45,7 +46,7 @@ inline BatchArgs batch_args(const KvCache& kv, const ar_batch_t& b, int window)
     int shift = 4;
     while ((1 << shift) < kv.d.page_size) ++shift;
     return BatchArgs{b.q_start, b.kv_len, b.page_table, b.table_stride, (int)b.tokens, b.seqs, shift,
-                     (int)kv.d.pages, window};
+                     (int)kv.d.pages, window, kv.h->persist_absent};
 }
 
 // What the attention kernels take beside the batch.

@@ -462,6 +462,28 @@ __device__ __forceinline__ bool wait_or_give_up(uint64_t* bar, uint32_t parity, 
     return false;
 }
 
+// Before a CTA ends, whoever issued asynchronous work of it waits for that work,
+// however the CTA's other waits ended: what is in flight still writes this CTA's
+// shared memory, which another CTA would own by then.
+__device__ __forceinline__ void wait_for_own(uint64_t* bar, uint32_t parity, DevStatus* st)
+{
+    if (!wait_a_second(bar, parity, nullptr)) report_wait_timeout(st);
+}
+
+// wait_for_own for a ring of `stages` that `issued` tiles went through; `stage` and
+// `phase` are the next tile's.  Usually the last tiles have long been waited for.
+__device__ __forceinline__ void wait_for_ring(uint64_t* full, int stages, uint32_t issued, int stage, uint32_t phase,
+                                              DevStatus* st)
+{
+    for (uint32_t k = 0; k < issued && k < (uint32_t)stages; ++k) {
+        if (--stage < 0) {
+            stage = stages - 1;
+            phase ^= 1;
+        }
+        wait_for_own(&full[stage], phase, st);
+    }
+}
+
 __device__ __forceinline__ float ex2(float x)
 {
     float y;

@@ -167,7 +167,10 @@ enum {
     AR_OPT_ABSENT_RANK = 14, /* failure emulation for ar_ring_persistent and ar_ring_cluster:
                                 rank r (0..n-1) never joins, so its neighbours' waits run out after
                                 AR_OPT_SPIN_NS and the status reads AR_ERR_FLAG_TIMEOUT or
-                                AR_ERR_WAIT_TIMEOUT; -1 (default): every rank takes part */
+                                AR_ERR_WAIT_TIMEOUT; for ar_paged_attention: rank r's keys never
+                                arrive, the waits for them run out after a second, rows are
+                                unspecified and the status reads AR_ERR_WAIT_TIMEOUT;
+                                -1 (default): every rank takes part */
     AR_OPT_TWO_SHOT_IMPL = 15,/* ar_two_shot's form, same bits and bytes: 1 two launches (the
                                 kernel boundary separates the phases); 2 one launch, each CTA
                                 gathering the tile it reduced after a CTA barrier; 3 one launch,
