@@ -27,8 +27,8 @@
 // may rescale O in place without another wait.
 //
 // Softmax in one pass, base 2, as in the decode kernel: the reference m moves only
-// when a row's maximum passes it by more than 8, so O is rescaled a few times at
-// the start of a row and hardly ever later.
+// when a row's maximum passes it by far (kSlack, kBelow), so O is rescaled a few times
+// at the start of a row and hardly ever later.
 //
 // Measured on GB300 (n = 8 bf16, heads of 128): 8192 tokens behind 8192 with 64
 // query heads 2.08 to 2.25 ms from run to run, 1470 to 1590 TFLOP/s (77 to 83%
@@ -53,7 +53,6 @@ constexpr int kTh = 384;
 // Registers a thread: 384 x 168 at launch = 256 x 200 + 128 x 104 (208 / 88: 2% slower,
 // 192 / 120: 1%).
 constexpr int kSoftmaxRegs = 200, kOtherRegs = 104;
-constexpr float kSlack = 8.0f;
 
 // weight of a row tile's start and end: 2 / 3 / 4 key tiles, packed prompts 208.5 / 204 /
 // 203.6 us, 117 tokens on 7752 keys 32.9 / 30.3 / 35.6 us
@@ -475,11 +474,11 @@ __device__ void soften(const ChunkArgs& a, const BatchArgs& b, ChunkShared* sh, 
 #pragma unroll
             for (int e = 0; e < 4; ++e) mx[e] = fmaxf(mx[e], s[kKeys - 4 + e]);
             const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * a.scale_log2;
-            const bool move = top > m + kSlack;
+            const bool move = top > m + (kSlack + kBelow<DT>);
             const bool rescale = __any_sync(0xffffffffu, move);
             float f = 1.0f;
             if (rescale) {
-                const float to = move ? top : m;
+                const float to = move ? top - kBelow<DT> : m;
                 f = m == -INFINITY ? 0.0f : ex2(m - to);
                 m = to;
                 float p, q, u, v;

@@ -24,8 +24,7 @@
 //
 // Softmax in one pass, base 2: with x = scale log2(e) (q . k), a running
 // reference m, p = 2^(x - m), l = sum p, o = sum p v.  m moves only when a row's
-// maximum passes it by more than 8: p stays below 2^8, which fp32 sums, fp16
-// and bf16 all hold without loss, and the accumulators are seldom rescaled.
+// maximum passes it by far (kSlack, kBelow), so the accumulators are seldom rescaled.
 //
 // Split of the keys: split_work cuts all key tiles of the call into equal runs,
 // one per CTA.  Row tiles that lie in several runs leave their parts (o, m, l,
@@ -39,7 +38,6 @@ namespace {
 constexpr int kKeys = 64;                    // keys of a tile
 constexpr int kWarps = 4;                    // consumers, 16 keys each
 constexpr int kTh = 32 * (kWarps + 1);
-constexpr float kSlack = 8.0f;               // log2 of how far p may pass 1
 
 // a row tile's start and end weigh a key tile more (0 / 1 / 2 / 3: 8 sequences of 700
 // keys 15.1 / 12.6 / 13.4 / 14.1 us, 64 of 1000 keys 59 / 55.5 / 53.5 / 53.0)
@@ -303,13 +301,13 @@ __device__ void consume(const DecodeArgs& a, const BatchArgs& b, const Cursor& c
                 for (int i = 0; i < 2; ++i) {
 #pragma unroll
                     for (int w = 0; w < SHARED; ++w) mx[i] = fmaxf(mx[i], __shfl_xor_sync(0xffffffffu, mx[i], FIRST << w));
-                    move |= mx[i] > m[i] + kSlack;
+                    move |= mx[i] > m[i] + (kSlack + kBelow<DT>);
                 }
                 if (__any_sync(0xffffffffu, move)) {
                     float f[2];
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
-                        const float to = fmaxf(m[i], mx[i]);
+                        const float to = fmaxf(m[i], mx[i] - kBelow<DT>);
                         f[i] = m[i] == -INFINITY ? 0.0f : ex2(m[i] - to);
                         m[i] = to;
                         l[i] *= f[i];
@@ -330,8 +328,9 @@ __device__ void consume(const DecodeArgs& a, const BatchArgs& b, const Cursor& c
                         l[i] += p[nt][e];
                     }
                 // The product's operand has the cache's type: p = high + low, both rounded to it, so that
-                // what is lost is a half step of a half step.  Rounded once, the outputs of short batches
-                // were off by 1.4 times their own rounding; the second product is hidden behind the copies.
+                // what is lost is a half step of a half step (fp16: or 2^-32 of the largest p, see kBelow).
+                // Rounded once, the outputs of short batches were off by 1.4 times their own rounding;
+                // the second product is hidden behind the copies.
                 uint32_t high[2 * NS], low[2 * NS];
 #pragma unroll
                 for (int nt = 0; nt < NS; ++nt)

@@ -491,6 +491,16 @@ __device__ __forceinline__ float ex2(float x)
     return y;
 }
 
+// The softmax's probabilities are p = 2^(x - m), x the scores in base 2, against a
+// reference m that is put kBelow under a row's maximum and moves only when one
+// passes it by kBelow + kSlack: the accumulators are seldom rescaled, and p stays
+// under 2^(kBelow + kSlack).  As the second product's operand p has the cache's type.
+// bf16 reaches as far down as fp32.  fp16 ends at 2^-24 (and has a fixed step of that
+// below 2^-14), but goes up to 2^16, so there the largest p is near 2^7 to 2^15 and not
+// 1: what is lost of a probability is at most 2^-32 of the largest.
+constexpr float kSlack = 8.0f;
+template <int DT> constexpr float kBelow = DT == AR_F16 ? 7.0f : 0.0f;
+
 // 16-byte chunk `c` of 128-byte row `r` of a panel written by a tensor copy
 // with the 128-byte swizzle (the panel starts on a multiple of 1024 bytes).
 __device__ __forceinline__ uint32_t swizzled(uint32_t panel, int r, int c)

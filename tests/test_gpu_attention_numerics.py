@@ -1,5 +1,6 @@
 """ar_paged_attention where its arithmetic can go wrong: NaN in queries and
-keys of sequences that are split over CTAs."""
+keys of sequences that are split over CTAs, and probabilities far below a row's
+largest."""
 
 import numpy as np
 import pytest
@@ -59,3 +60,38 @@ def test_nan_keys_reach_every_row_that_sees_them(first, last, max_new):
         q, out = run(L, heads)
         nan_rows = {(r, 0, i, h) for r in range(2) for i in range(2) for h in range(heads)}
         compare_but(L, q, out, heads, nan_rows)
+
+
+@KERNELS
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("below", [16.0, 25.0, 26.5, 30.0])   # powers of two
+def test_weights_far_below_the_largest_still_count(below, dim, max_new):
+    """A first key that takes nearly all weight and whose value is 0 (an
+    attention sink): the output is what the others' weights, 2^-below each, make
+    of their values.  fp16 has no number below 2^-24.  Per key the operand may be
+    off by half of that against a largest weight of at least 2^7, so by
+    2^-25 2^-7 |v| of the output, beside what `expect` counts."""
+    heads, keys = 2, [5000, 60]
+    with Layer(2, 1, dim, 64, "f16", [1, 1], keys, max_new=max_new) as L:
+        q = L.rows(heads)
+        for r in range(L.n):
+            q[r][: L.tokens, 0: heads * dim: dim] = 8.0
+            for s, n in enumerate(keys):
+                k, v = L.keys[r][s], L.vals[r][s].abs() + 0.5
+                k *= 2.0**-6
+                k[:, :, 0] = 0.0
+                k[0] = 0.0
+                k[0, :, 0] = below / np.log2(np.e) * dim**0.5 / 8
+                v[0] = 0.0
+                L.vals[r][s] = v
+                for j in range(0, n, L.page):
+                    p, m = int(L.table[s, j // L.page]), min(L.page, n - j)
+                    L.kview[r][p, :, :m] = k[j: j + m].transpose(0, 1).cuda()
+                    L.vview[r][p, :, :m] = v[j: j + m].transpose(0, 1).cuda()
+        q, out = run(L, heads, q=q)
+        for r in range(L.n):
+            for s, n in enumerate(keys):
+                want, tol = expect(L, q, heads, dim**-0.5, 0, r, s)
+                got = rows_of(L, out, heads, r, s)
+                tol = tol + n * 2.0**-32 * f64(L.vals[r][s]).max()
+                assert (np.abs(got - want) <= tol).all(), (r, s, got[0, 0, :4], want[0, 0, :4], tol[0, 0, :4])
