@@ -70,19 +70,31 @@ struct Span {
 };
 
 template <int KT>
-__device__ __forceinline__ Span span_of(const Seq& q, int tm, int t, int window)
+__host__ __device__ __forceinline__ Span span_of(const Seq& q, int tm, int t, int window)
 {
     const int first = q.c0 + t * tm;                                // position of the tile's first token
-    const int last = q.c0 + min((t + 1) * tm, q.nq);                // one past its last token's position
+    const int end = (t + 1) * tm, last = q.c0 + (end < q.nq ? end : q.nq);   // one past its last token's position
     Span p;
-    p.key_hi = max(last, 0);
-    p.key_lo = window > 0 ? max(first - window + 1, 0) : 0;
+    p.key_hi = last > 0 ? last : 0;
+    p.key_lo = window > 0 && first - window + 1 > 0 ? first - window + 1 : 0;
     p.j_lo = p.key_lo / KT;
-    p.tiles = max((p.key_hi + KT - 1) / KT - p.j_lo, 1);
+    const int tiles = (p.key_hi + KT - 1) / KT - p.j_lo;
+    p.tiles = tiles > 1 ? tiles : 1;
     return p;
 }
 
 typedef unsigned long long u64;
+
+// Units of all row tiles of a sequence; a long prompt has more than 2^32 (a million
+// tokens, one to a row tile, 64 keys to a key tile: 2^33).
+template <typename S>
+__host__ __device__ __forceinline__ u64 units_of_sequence(const Seq& q, int tm, int window)
+{
+    u64 sum = 0;
+    const int nt = (q.nq + tm - 1) / tm;
+    for (int t = 0; t < nt; ++t) sum += (u64)(span_of<S::KT>(q, tm, t, window).tiles + S::W);
+    return sum;
+}
 
 struct Cursor {
     u64 begin;                   // first unit of the current triple
@@ -177,12 +189,7 @@ __device__ bool split_few(const BatchArgs& b, int tm, int heads, int min_units, 
 {
     const int lane = threadIdx.x & 31;
     const int per = (b.seqs + 31) / 32, s0 = min(lane * per, b.seqs), s1 = min(s0 + per, b.seqs);
-    auto units_in = [&](const Seq& q) {
-        unsigned sum = 0;
-        const int nt = (q.nq + tm - 1) / tm;
-        for (int t = 0; t < nt; ++t) sum += (unsigned)(span_of<S::KT>(q, tm, t, b.window).tiles + S::W);
-        return sum;
-    };
+    auto units_in = [&](const Seq& q) { return units_of_sequence<S>(q, tm, b.window); };
     u64 mine = 0;
     Seq q{0, 0, 0, 0};
     if (per == 1) {
@@ -215,7 +222,7 @@ __device__ bool split_few(const BatchArgs& b, int tm, int heads, int min_units, 
     if (per > 1 && lane == src)
         for (;; ++s) {
             q = load_seq(b, s, st);
-            const unsigned u = units_in(q);
+            const u64 u = units_in(q);
             if (off < u) break;
             off -= u;
         }
@@ -250,8 +257,7 @@ __device__ bool split_work(const BatchArgs& b, int tm, int heads, int min_units,
         if (s < s1) q = load_seq(b, s, st);
         const int nt = (q.nq + tm - 1) / tm;
         const bool is_long = nt > 8;
-        if (!is_long)
-            for (int t = 0; t < nt; ++t) mine += units_of(q, t);
+        if (!is_long) mine += units_of_sequence<S>(q, tm, b.window);
         unsigned todo = __ballot_sync(0xffffffffu, is_long);
         while (todo) {
             const int src = __ffs(todo) - 1;
@@ -289,11 +295,7 @@ __device__ bool split_work(const BatchArgs& b, int tm, int heads, int min_units,
         u64 at = excl;
         for (int s = s0; s < s1; ++s) {
             u64 sum = 0;
-            if (s + 1 < s1) {
-                const Seq q = load_seq(b, s, st);
-                const int nt = (q.nq + tm - 1) / tm;
-                for (int t = 0; t < nt; ++t) sum += units_of(q, t);
-            }
+            if (s + 1 < s1) sum = units_of_sequence<S>(load_seq(b, s, st), tm, b.window);
             if (s + 1 == s1 || in_head < at + sum) {
                 sh->s = s;
                 sh->off = in_head - at;
