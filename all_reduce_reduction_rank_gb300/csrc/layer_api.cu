@@ -50,7 +50,8 @@ int check_desc(const ar_kv_desc_t* d)
 int check_batch(const ar_batch_t* b)
 {
     if (!b) return AR_ERR_INVALID;
-    if (b->seqs < 0 || b->tokens > (size_t)1 << 30) return AR_ERR_INVALID;
+    // the kernels look a little past the last sequence in 32 bits before they compare
+    if (b->seqs < 0 || b->seqs > 1 << 30 || b->tokens > (size_t)1 << 30) return AR_ERR_INVALID;
     if (b->tokens == 0) return AR_OK;
     if (b->seqs == 0 || b->max_new < 1) return AR_ERR_INVALID;
     if (!b->q_start || !b->kv_len || !b->page_table) return AR_ERR_INVALID;

@@ -539,7 +539,7 @@ int ar_kv_destroy(ar_kv kv);
  * reads AR_ERR_INDEX. */
 typedef struct {
     size_t tokens;             /* new tokens in all, at most 2^30 */
-    int seqs;
+    int seqs;                  /* sequences, at most 2^30 */
     int max_new;               /* most new tokens of one sequence: chooses the kernel, never the result */
     const int32_t* q_start;    /* [seqs + 1] */
     const int32_t* kv_len;     /* [seqs] */

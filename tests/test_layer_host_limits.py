@@ -1,0 +1,14 @@
+"""Limits of the layer's calls that only show at their ends, without a GPU."""
+
+import pytest
+
+import all_reduce_reduction_rank_gb300 as ar
+from test_layer_host import append, attention, batch, lib  # noqa: F401  (lib: builds and loads the library)
+
+
+def test_sequences_are_counted_below_2_30():
+    # kernels form indices a little past the last sequence in 32 bits
+    for seqs in ((1 << 30) + 1, 2**31 - 1):
+        assert attention(batch(seqs=seqs)) == ar.AR_ERR_INVALID
+        assert append(batch(seqs=seqs)) == ar.AR_ERR_INVALID
+    assert attention(batch(seqs=1 << 30)) == ar.AR_OK and append(batch(seqs=1 << 30)) == ar.AR_OK
