@@ -18,6 +18,8 @@ namespace {
 
 constexpr uint32_t kKvMagic = 0x41524b56u;  // "ARKV"
 
+constexpr size_t kMaxStride = (size_t)1 << 39;   // elements: tensor copies take strides below 2^40 bytes
+
 bool aligned16(const void* p) { return ((uintptr_t)p & 15u) == 0; }
 
 // Runs f on the handle's device, restoring the caller's device after.
@@ -40,9 +42,8 @@ int check_desc(const ar_kv_desc_t* d)
     if (d->head_dim != 64 && d->head_dim != 128) return AR_ERR_INVALID;
     if (d->page_size != 16 && d->page_size != 32 && d->page_size != 64 && d->page_size != 128) return AR_ERR_INVALID;
     if (d->pages < 1 || d->pages > (size_t)INT_MAX) return AR_ERR_INVALID;
-    // tensor copies take strides below 2^40 bytes
     for (size_t st : {d->page_stride, d->head_stride, d->token_stride})
-        if (st == 0 || st % 8 != 0 || st >= (size_t)1 << 39) return AR_ERR_INVALID;
+        if (st == 0 || st % 8 != 0 || st >= kMaxStride) return AR_ERR_INVALID;
     if (d->token_stride < (size_t)d->head_dim) return AR_ERR_INVALID;
     return AR_OK;
 }
@@ -66,7 +67,8 @@ int check_rows(int n, const void* const* p, size_t row, size_t stride, size_t to
     if (!p) return AR_ERR_INVALID;
     for (int r = 0; r < n; ++r)
         if (!p[r]) return AR_ERR_INVALID;
-    if (stride < row || stride % 8 != 0 || stride > ((size_t)1 << 40) / (tokens ? tokens : 1)) return AR_ERR_INVALID;
+    if (stride < row || stride % 8 != 0 || stride >= kMaxStride || stride > ((size_t)1 << 40) / (tokens ? tokens : 1))
+        return AR_ERR_INVALID;
     for (int r = 0; r < n; ++r)
         if (!aligned16(p[r])) return AR_ERR_ALIGN;
     return AR_OK;

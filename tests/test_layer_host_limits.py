@@ -12,3 +12,11 @@ def test_sequences_are_counted_below_2_30():
         assert attention(batch(seqs=seqs)) == ar.AR_ERR_INVALID
         assert append(batch(seqs=seqs)) == ar.AR_ERR_INVALID
     assert attention(batch(seqs=1 << 30)) == ar.AR_OK and append(batch(seqs=1 << 30)) == ar.AR_OK
+
+
+def test_row_strides_fit_a_tensor_copy():
+    # the chunk kernel's copies of the queries take strides below 2^40 bytes
+    for stride in (1 << 39, 1 << 40):
+        assert attention(batch(tokens=1, seqs=1), qs=stride) == ar.AR_ERR_INVALID
+        assert append(batch(tokens=1, seqs=1), qs=stride) == ar.AR_ERR_INVALID
+    assert attention(batch(tokens=1, seqs=1), qs=(1 << 39) - 8) == ar.AR_OK
