@@ -754,7 +754,7 @@ int launch_attention_chunk(KvCache& kv, const ar_batch_t& b, const AttnCall& c, 
     a.partial = kv.partial;
     a.joins = static_cast<JoinWork*>(kv.joins);
     a.out_stride = c.out_stride;
-    a.scale_log2 = c.scale * 1.4426950408889634f;
+    a.scale_log2 = c.scale * kLog2e;
     a.n = h.n;
     a.kv_heads = kv.d.kv_heads;
     a.group = group;

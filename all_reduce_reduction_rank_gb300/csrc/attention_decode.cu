@@ -577,7 +577,7 @@ int launch_attention_decode(KvCache& kv, const ar_batch_t& b, const AttnCall& c,
     a.arrived = kv.arrived;
     a.q_stride = c.q_stride;
     a.out_stride = c.out_stride;
-    a.scale_log2 = c.scale * 1.4426950408889634f;
+    a.scale_log2 = c.scale * kLog2e;
     a.n = h.n;
     a.kv_heads = kv.d.kv_heads;
     a.group = c.q_heads / kv.d.kv_heads;

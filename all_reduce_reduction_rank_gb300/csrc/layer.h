@@ -11,6 +11,7 @@ namespace argb {
 
 constexpr int kAttnTileRows = 128;   // query rows of one tensor-core tile of the chunk kernel
 constexpr int kMaxGroup = 64;        // query heads per kv head
+constexpr float kLog2e = 1.4426950408889634f;   // the kernels' exponentials are powers of two
 
 // The registered caches of a handle's ranks (ar_kv).
 struct KvCache {

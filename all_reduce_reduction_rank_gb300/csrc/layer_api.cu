@@ -136,7 +136,7 @@ int check_attention(int n, const ar_kv_desc_t& d, const ar_batch_t* b, const Att
 {
     if (int rc = check_batch(b)) return rc;
     if (c.q_heads < 1 || c.q_heads % d.kv_heads != 0 || c.q_heads / d.kv_heads > kMaxGroup) return AR_ERR_INVALID;
-    if (!(c.scale > 0.0f) || c.scale == INFINITY || window < 0) return AR_ERR_INVALID;
+    if (!(c.scale > 0.0f) || !std::isfinite(c.scale * kLog2e) || window < 0) return AR_ERR_INVALID;
     const size_t row = (size_t)d.head_dim * (size_t)c.q_heads;
     if (int rc = check_rows(n, c.q, row, c.q_stride, b->tokens)) return rc;
     if (int rc = check_rows(n, c.out, row, c.out_stride, b->tokens)) return rc;

@@ -588,7 +588,8 @@ int ar_rope_append(ar_kv kv, const ar_batch_t* batch, const void* const* q, cons
  * split follows the batch alone, and its parts are joined in one order).
  * ar_traffic reports the queries' and outputs' bytes: the keys are known on the
  * device only.
- * q_heads is a multiple of kv_heads, at most 64 times it; scale is finite and > 0. */
+ * q_heads is a multiple of kv_heads, at most 64 times it; scale is > 0 and
+ * scale * log2(e) finite in fp32. */
 int ar_paged_attention(ar_kv kv, const ar_batch_t* batch, const void* const* q, void* const* out, int q_heads,
                        size_t q_stride, size_t out_stride, float scale, int window, ar_stream_t stream);
 

@@ -20,3 +20,10 @@ def test_row_strides_fit_a_tensor_copy():
         assert attention(batch(tokens=1, seqs=1), qs=stride) == ar.AR_ERR_INVALID
         assert append(batch(tokens=1, seqs=1), qs=stride) == ar.AR_ERR_INVALID
     assert attention(batch(tokens=1, seqs=1), qs=(1 << 39) - 8) == ar.AR_OK
+
+
+def test_the_scale_is_finite_in_base_2_too():
+    # scores are scaled by scale * log2(e), which fp32 must hold
+    assert attention(scale=2.3e38) == ar.AR_OK
+    for bad in (2.4e38, 3.4e38):
+        assert attention(scale=bad) == ar.AR_ERR_INVALID
