@@ -1,9 +1,8 @@
 """Limits of the layer's calls that only show at their ends, without a GPU."""
 
-import pytest
 
 import all_reduce_reduction_rank_gb300 as ar
-from test_layer_host import append, attention, batch, lib  # noqa: F401  (lib: builds and loads the library)
+from test_layer_host import append, at, attention, batch, desc, lib  # noqa: F401  (lib: builds and loads the library)
 
 
 def test_sequences_are_counted_below_2_30():
@@ -27,3 +26,11 @@ def test_the_scale_is_finite_in_base_2_too():
     assert attention(scale=2.3e38) == ar.AR_OK
     for bad in (2.4e38, 3.4e38):
         assert attention(scale=bad) == ar.AR_ERR_INVALID
+
+
+def test_caches_fit_an_address_space():
+    # the kernels form page * page_stride in 64 bits
+    ok = lambda d: ar.ar_check_kv(4, d, at(0), at(1))
+    assert ok(desc(pages=1 << 20, ps=1 << 38)) == ar.AR_OK
+    for bad in ({"pages": 2**31 - 1, "ps": 1 << 38}, {"pages": 1 << 25, "ps": 1 << 38}):
+        assert ok(desc(**bad)) == ar.AR_ERR_INVALID, bad
