@@ -45,8 +45,8 @@ int check_desc(const ar_kv_desc_t* d)
     for (size_t st : {d->page_stride, d->head_stride, d->token_stride})
         if (st == 0 || st % 8 != 0 || st >= kMaxStride) return AR_ERR_INVALID;
     if (d->token_stride < (size_t)d->head_dim) return AR_ERR_INVALID;
-    // no cache is longer than an address space (2^57 bytes), and page * page_stride fits 64 bits
-    if (d->pages - 1 > (((size_t)1 << 56) - 1) / d->page_stride) return AR_ERR_INVALID;
+    // page * page_stride fits 64 bits by far (no address space has 2^59 bytes)
+    if (d->pages - 1 > ((size_t)1 << 58) / d->page_stride) return AR_ERR_INVALID;
     return AR_OK;
 }
 

@@ -1,6 +1,5 @@
 """Limits of the layer's calls that only show at their ends, without a GPU."""
 
-
 import all_reduce_reduction_rank_gb300 as ar
 from test_layer_host import append, at, attention, batch, desc, lib  # noqa: F401  (lib: builds and loads the library)
 
