@@ -54,7 +54,7 @@ EXPORTS = (
     "ar_one_shot_push", "ar_one_shot_copyin", "ar_ring_rounded", "ar_tree", "ar_ring_persistent",
     "ar_ring_cluster", "ar_tree_fused", "ar_ring_fused", "ar_ring_rounded_fused", "ar_allreduce_block_norm",
     "ar_kv_create", "ar_kv_destroy", "ar_rope_append", "ar_paged_attention", "ar_check_block_norm", "ar_check_kv",
-    "ar_check_rope_append", "ar_check_paged_attention",
+    "ar_check_rope_append", "ar_check_paged_attention", "ar_check_rows_apart",
 )
 
 
@@ -143,6 +143,7 @@ def lib() -> ctypes.CDLL:
                                           sz, sz, sz, vp, sz, i32, i32], i32),
                 "ar_check_paged_attention": ([i32, ctypes.POINTER(KvDesc), ctypes.POINTER(Batch), pp, pp, i32, sz,
                                               sz, ctypes.c_float, i32], i32),
+                "ar_check_rows_apart": ([i32, ctypes.POINTER(KvDesc), pp, pp, pp, sz, sz, sz], i32),
                 "ar_one_shot_push": ([vp, pp, pp, sz, i32, vp], i32),
                 "ar_one_shot_copyin": ([vp, pp, pp, sz, i32, vp], i32),
                 "ar_ring_rounded": ([vp, pp, pp, sz, i32, vp], i32),
@@ -454,6 +455,11 @@ def ar_check_paged_attention(n_ranks: int, desc: KvDesc, batch: Batch, qs, outs,
                              out_stride: int, scale: float, window: int = 0) -> int:
     return lib().ar_check_paged_attention(n_ranks, ctypes.byref(desc), ctypes.byref(batch), _ptr_array(qs),
                                           _ptr_array(outs), q_heads, q_stride, out_stride, scale, window)
+
+
+def ar_check_rows_apart(n_ranks: int, desc: KvDesc, ks, vs, rows, row: int, stride: int, tokens: int) -> int:
+    return lib().ar_check_rows_apart(n_ranks, ctypes.byref(desc), _ptr_array(ks), _ptr_array(vs), _ptr_array(rows),
+                                     row, stride, tokens)
 
 
 def ar_timing(h, max_records: int = 1 << 20) -> list[tuple[str, int, float, int, int]]:

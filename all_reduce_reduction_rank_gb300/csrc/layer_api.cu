@@ -6,6 +6,7 @@
 #include <cmath>
 #include <cstring>
 #include <new>
+#include <utility>
 
 #include <cudaTypedefs.h>
 
@@ -87,6 +88,47 @@ bool rows_overlap(const void* a, size_t ea, size_t sa, const void* b, size_t eb,
     if (sa != sb) return true;
     const size_t s = sa * 2, at = x >= y ? (x - y) % s : (s - (y - x) % s) % s;   // a's place in b's rows
     return at < eb * 2 || at + ea * 2 > s;
+}
+
+// `count` blocks of `width` bytes, `stride` apart.
+struct Blocks {
+    uintptr_t at;
+    size_t width, stride, count;
+    uintptr_t end() const { return at + (count - 1) * stride + width; }
+};
+
+// Some block of a and some block of b share a byte.
+bool blocks_meet(Blocks a, Blocks b)
+{
+    if (a.count > b.count) std::swap(a, b);
+    for (size_t i = 0; i < a.count; ++i) {
+        const uintptr_t lo = a.at + i * a.stride, hi = lo + a.width;
+        if (hi <= b.at) continue;
+        const size_t j = std::min((size_t)(hi - 1 - b.at) / b.stride, b.count - 1);   // the last that begins before hi
+        if (b.at + j * b.stride + b.width > lo) return true;
+    }
+    return false;
+}
+
+// The caches' pages and n buffers of rows.  A page counts with what lies between
+// its slots and heads.
+int check_apart(int n, const ar_kv_desc_t& d, void* const* k, void* const* v, const void* const* rows, size_t row,
+                size_t stride, size_t tokens)
+{
+    if (tokens == 0) return AR_OK;
+    const size_t page = ((size_t)d.kv_heads - 1) * d.head_stride + ((size_t)d.page_size - 1) * d.token_stride +
+                        (size_t)d.head_dim;
+    const size_t length = Blocks{0, 2 * page, 2 * d.page_stride, d.pages}.end();
+    for (int r = 0; r < n; ++r) {
+        const Blocks x{(uintptr_t)rows[r], 2 * row, 2 * stride, tokens};
+        const uintptr_t lo = x.at, hi = x.end();
+        for (int c = 0; c < 2 * n; ++c) {
+            const uintptr_t at = (uintptr_t)(c < n ? k[c] : v[c - n]);
+            if (lo >= at + length || at >= hi) continue;   // buffers that lie apart, as usual
+            if (blocks_meet(x, Blocks{at, 2 * page, 2 * d.page_stride, d.pages})) return AR_ERR_INVALID;
+        }
+    }
+    return AR_OK;
 }
 
 int check_kv(int n, const ar_kv_desc_t* d, void* const* k, void* const* v)
@@ -256,6 +298,14 @@ int ar_check_kv(int n_ranks, const ar_kv_desc_t* desc, void* const* k, void* con
     return check_kv(n_ranks, desc, k, v);
 }
 
+int ar_check_rows_apart(int n_ranks, const ar_kv_desc_t* desc, void* const* k, void* const* v,
+                        const void* const* rows, size_t row, size_t stride, size_t tokens)
+{
+    if (int rc = check_kv(n_ranks, desc, k, v)) return rc;
+    if (int rc = check_rows(n_ranks, rows, row, stride, tokens)) return rc;
+    return check_apart(n_ranks, *desc, k, v, rows, row, stride, tokens);
+}
+
 int ar_check_rope_append(int n_ranks, const ar_kv_desc_t* desc, const ar_batch_t* b, const void* const* q,
                          const void* const* k, const void* const* v, void* const* q_out, int q_heads, size_t q_stride,
                          size_t kv_stride, size_t q_out_stride, const float* cos_sin, size_t max_positions,
@@ -303,6 +353,15 @@ int ar_rope_append(ar_kv k, const ar_batch_t* b, const void* const* q, const voi
     const RopeCall c{q, kn, vn, q_out, q_heads, q_stride, kv_stride, q_out_stride, cos_sin, max_positions, rot_dim,
                      interleaved};
     if (int rc = check_rope(h.n, kv->d, b, c)) return rc;
+    const auto apart = [&](const void* const* rows, int heads, size_t stride) {
+        return check_apart(h.n, kv->d, kv->k, kv->v, rows, (size_t)kv->d.head_dim * heads, stride, b->tokens);
+    };
+    if (int rc = apart(kn, kv->d.kv_heads, kv_stride)) return rc;
+    if (int rc = apart(vn, kv->d.kv_heads, kv_stride)) return rc;
+    if (q) {
+        if (int rc = apart(q, q_heads, q_stride)) return rc;
+        if (int rc = apart(q_out, q_heads, q_out_stride)) return rc;
+    }
     const size_t row = (size_t)kv->d.head_dim * ((size_t)(q ? q_heads : 0) + 2u * (size_t)kv->d.kv_heads);
     int rc = AR_OK;
     h.timing.op = AR_OP_ROPE_APPEND;
@@ -322,6 +381,7 @@ int ar_paged_attention(ar_kv k, const ar_batch_t* b, const void* const* q, void*
     const AttnCall c{q, out, q_heads, q_stride, out_stride, scale};
     if (int rc = check_attention(h.n, kv->d, b, c, window)) return rc;
     const size_t row = (size_t)kv->d.head_dim * (size_t)q_heads;
+    if (int rc = check_apart(h.n, kv->d, kv->k, kv->v, out, row, out_stride, b->tokens)) return rc;
     int rc = AR_OK;
     h.timing.op = AR_OP_PAGED_ATTENTION;
     // Rows of a sequence per kv head.  The decode kernel reads the keys again for every 16 of

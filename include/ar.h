@@ -559,8 +559,8 @@ typedef struct {
  *   q_heads (kv_heads) heads of head_dim, q_stride / kv_stride / q_out_stride
  *   elements apart (multiples of 8), 16-byte aligned: slices of one packed
  *   projection are fine.  q and q_out may both be NULL (keys and values only)
- *   and q_out[r] may equal q[r] with equal strides; no other output may
- *   overlap an input.
+ *   and q_out[r] may equal q[r] with equal strides; no other output, the
+ *   caches among them, may overlap an input or another output.
  * A token whose position is not in 0 .. max_positions - 1 (when R > 0), or
  * whose page is out of range, is left out and sets AR_ERR_INDEX. */
 int ar_rope_append(ar_kv kv, const ar_batch_t* batch, const void* const* q, const void* const* k,
@@ -575,7 +575,7 @@ int ar_rope_append(ar_kv kv, const ar_batch_t* batch, const void* const* q, cons
  * with query head h on kv head h / (q_heads / kv_heads).  A token that sees no
  * key (position < 0) gets 0.  q and out: host arrays of n_ranks device pointers
  * to rows of q_heads heads of head_dim, q_stride / out_stride elements apart
- * (multiples of 8), 16-byte aligned, not overlapping.  The caches already hold
+ * (multiples of 8), 16-byte aligned, not overlapping, out not in the caches.  The caches already hold
  * the new tokens (ar_rope_append); cache slots at or past kv_len, and before
  * the window of a sequence's first new token, may hold anything, NaN included.
  * A non-finite value within them may reach every row of the sequence.
@@ -717,7 +717,10 @@ int ar_check_args(int op, int n_ranks, size_t max_bytes, const void* const* in,
  * ar_kv_create, ar_rope_append and ar_paged_attention would return for these
  * arguments before launching anything (desc: as given to ar_kv_create).
  * Pointers are compared, never dereferenced, the batch's device arrays among
- * them. */
+ * them.  Of the caches they are given the description alone: that no row of q, k,
+ * v or q_out (append), of out (attention) lies in a page of them is what
+ * ar_check_rows_apart says of n_ranks buffers of rows of `row` elements.  A page
+ * counts with what lies between its slots and heads. */
 int ar_check_block_norm(int n_ranks, size_t max_bytes, const void* const* in, const ar_block_norm_t* p,
                         void* const* norm_out, void* residual_out, size_t tokens, size_t hidden, ar_dtype dt);
 int ar_check_kv(int n_ranks, const ar_kv_desc_t* desc, void* const* k, void* const* v);
@@ -728,6 +731,9 @@ int ar_check_rope_append(int n_ranks, const ar_kv_desc_t* desc, const ar_batch_t
 int ar_check_paged_attention(int n_ranks, const ar_kv_desc_t* desc, const ar_batch_t* batch, const void* const* q,
                              void* const* out, int q_heads, size_t q_stride, size_t out_stride, float scale,
                              int window);
+
+int ar_check_rows_apart(int n_ranks, const ar_kv_desc_t* desc, void* const* k, void* const* v,
+                        const void* const* rows, size_t row, size_t stride, size_t tokens);
 
 /* Static text for a return code. */
 const char* ar_strerror(int code);

@@ -33,3 +33,36 @@ def test_caches_fit_an_address_space():
     assert ok(desc(pages=1 << 20, ps=1 << 38)) == ar.AR_OK
     for bad in ({"pages": 2**31 - 1, "ps": 1 << 38}, {"pages": 1 << 25, "ps": 1 << 38}):
         assert ok(desc(**bad)) == ar.AR_ERR_INVALID, bad
+
+
+def apart(rows, d=None, ks=None, vs=None, row=1024, stride=1024, tokens=5):
+    return ar.ar_check_rows_apart(4, d or desc(), ks or at(0), vs or at(1), rows, row, stride, tokens)
+
+
+def test_rows_in_a_cache_are_refused():
+    page = 2 * 16 * 128 * 2                       # bytes of a page of desc(), 100 of them
+    assert apart(at(2)) == ar.AR_OK and apart(at(0, 100 * page)) == ar.AR_OK and apart(at(0), tokens=0) == ar.AR_OK
+    for off in (0, 16, 50 * page, 100 * page - 16):
+        assert apart(at(0, off)) == ar.AR_ERR_INVALID and apart(at(1, off)) == ar.AR_ERR_INVALID
+    for off in (-5 * 2048 + 16, -16):             # rows that begin before a cache and end in it
+        assert apart(at(0, off)) == ar.AR_ERR_INVALID
+    assert apart(at(0, -5 * 2048)) == ar.AR_OK
+    for r in range(4):                            # one rank's rows in another rank's cache
+        rows = at(2)
+        rows[r] = at(1)[(r + 1) % 4] + 4 * page
+        assert apart(rows) == ar.AR_ERR_INVALID
+    assert apart(at(0, 8)) == ar.AR_ERR_ALIGN and apart(at(2), stride=1000) == ar.AR_ERR_INVALID
+
+
+def test_rows_between_the_pages_of_a_cache_are_apart():
+    # one allocation of pages with room behind each: [page][2 x 16 x 128 of K, as much of V, 2048 elements more]
+    d = desc(ps=2 * 4096 + 2048)
+    step = 2 * (2 * 4096 + 2048)
+    vs, rows = at(0, 2 * 4096), at(0, 4 * 4096)
+    assert ar.ar_check_kv(4, d, at(0), vs) == ar.AR_OK
+    for tokens in (1, 5, 100, 130):               # more and fewer rows than pages, one row behind a page
+        assert apart(rows, d, vs=vs, stride=step // 2, tokens=tokens) == ar.AR_OK
+        assert apart([p + 2048 + 16 for p in rows], d, vs=vs, stride=step // 2, tokens=tokens) == (
+            ar.AR_ERR_INVALID if tokens > 0 else ar.AR_OK)
+    # rows that follow one another reach the next page
+    assert apart(rows, d, vs=vs, tokens=2) == ar.AR_OK and apart(rows, d, vs=vs, tokens=3) == ar.AR_ERR_INVALID
