@@ -583,7 +583,9 @@ __device__ void soften(const ChunkArgs& a, const BatchArgs& b, ChunkShared* sh, 
 #pragma unroll
                     for (int e = 0; e < 32; ++e) __stcg(part + (k + e) * kHalf + row, o[e]);
                 }
-            __stcg(part + D * kHalf + row, m);
+            // NaN scores never move m.  Where all are NaN it would still say that the part saw nothing,
+            // and the row would not come out as NaN as it does when it is not split
+            __stcg(part + D * kHalf + row, l != l ? 0.0f : m);
             __stcg(part + (D + 1) * kHalf + row, l);
             if (seg.slot & 1) {   // the first part
                 if (row == 0) {
@@ -697,7 +699,7 @@ attention_join_kernel(const __grid_constant__ ChunkArgs a)
         for (int k = 0; k < 4; ++k) {
             const float* from = part_of(min(k0 + k, j.parts - 1));
             m[k] = k0 + k < j.parts ? __ldcg(from + D * kHalf) : -INFINITY;
-            l[k] = k0 + k < j.parts ? __ldcg(from + (D + 1) * kHalf) : 0.0f;
+            l[k] = __ldcg(from + (D + 1) * kHalf);
 #pragma unroll
             for (int e = 0; e < kJoinColumns; ++e) x[k][e] = __ldcg(from + (d + e) * kHalf);
         }
@@ -709,11 +711,9 @@ attention_join_kernel(const __grid_constant__ ChunkArgs a)
         for (int e = 0; e < kJoinColumns; ++e) o[e] *= f;
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-            // a part that saw nothing (l = 0) may have written no columns: whatever is there does not
-            // count.  One that saw nothing but NaN scores never moved its m either, and its l is NaN:
-            // it counts, so that the row's result is NaN as in a row that was not split
-            const bool saw = m[k] != -INFINITY || l[k] != 0.0f;
-            const float w = m[k] != -INFINITY ? ex2(m[k] - to) : 1.0f;
+            // a part that saw nothing wrote no columns: whatever is there does not count
+            const bool saw = m[k] != -INFINITY;
+            const float w = saw ? ex2(m[k] - to) : 0.0f;
             sum = fmaf(saw ? l[k] : 0.0f, w, sum);
 #pragma unroll
             for (int e = 0; e < kJoinColumns; ++e) o[e] = fmaf(saw ? x[k][e] : 0.0f, w, o[e]);
