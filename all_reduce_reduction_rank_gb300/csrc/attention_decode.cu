@@ -581,12 +581,11 @@ int launch_attention_decode(KvCache& kv, const ar_batch_t& b, const AttnCall& c,
     a.n = h.n;
     a.kv_heads = kv.d.kv_heads;
     a.group = c.q_heads / kv.d.kv_heads;
-    // rows of a sequence per head group: 8 if they all fit
-    const bool eight = (size_t)b.max_new * (size_t)a.group <= 8;
-    const int rows = eight ? 8 : 16;
-    a.tile_heads = a.group < rows ? a.group : rows;
-    a.head_groups = (a.group + a.tile_heads - 1) / a.tile_heads;
-    a.tm = rows / a.tile_heads;
+    const DecodeTiles tiles = decode_tiles(a.group, b.max_new);
+    const bool eight = tiles.rows == 8;
+    a.tile_heads = tiles.heads;
+    a.head_groups = tiles.head_groups;
+    a.tm = tiles.tokens;
     a.box_tokens = kv.box_tokens;
     a.min_units = 2;
     a.few = b.seqs <= 256 && (b.max_new + a.tm - 1) / a.tm <= 8;

@@ -87,6 +87,26 @@ struct RopeCall {
 };
 int launch_rope_append(KvCache& kv, const ar_batch_t& b, const RopeCall& c, cudaStream_t s);
 
+// The decode kernel's row tiles: whole tokens of up to 16 query heads of a kv head, 8
+// rows if all rows of a sequence fit, else 16.
+struct DecodeTiles {
+    int rows;                        // 8 or 16
+    int heads, head_groups;          // query heads of a tile, tiles that a kv head's take
+    int tokens;                      // new tokens of a tile
+    size_t passes;                   // how often the keys of a sequence with max_new new tokens are read
+};
+
+inline DecodeTiles decode_tiles(int group, int max_new)
+{
+    DecodeTiles t;
+    t.rows = (size_t)max_new * (size_t)group <= 8 ? 8 : 16;
+    t.heads = group < t.rows ? group : t.rows;
+    t.head_groups = (group + t.heads - 1) / t.heads;
+    t.tokens = t.rows / t.heads;
+    t.passes = ((size_t)max_new + t.tokens - 1) / t.tokens * t.head_groups;
+    return t;
+}
+
 size_t attention_decode_partial_floats(const Handle& h, int head_dim);
 size_t attention_decode_counters(const Handle& h);
 size_t attention_chunk_partial_floats(const Handle& h, int head_dim);

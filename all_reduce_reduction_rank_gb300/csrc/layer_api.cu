@@ -384,12 +384,14 @@ int ar_paged_attention(ar_kv k, const ar_batch_t* b, const void* const* q, void*
     if (int rc = check_apart(h.n, kv->d, kv->k, kv->v, out, row, out_stride, b->tokens)) return rc;
     int rc = AR_OK;
     h.timing.op = AR_OP_PAGED_ATTENTION;
-    // Rows of a sequence per kv head.  The decode kernel reads the keys again for every 16 of
-    // them, the chunk kernel computes 256 whatever there is.  Measured on GB300 (n = 4, 2 kv heads,
-    // 64 sequences of 2000 keys, us, decode / chunk): heads of 128, 16 rows 94 / 116, 32 rows
-    // 167 / 117; heads of 64, 32 rows 91 / 96, 64 rows 165 / 96.
-    const size_t rows = (size_t)b->max_new * (size_t)(q_heads / kv->d.kv_heads);
-    const bool few = rows <= (kv->d.head_dim == 64 ? 32u : 16u);
+    // The decode kernel reads a sequence's keys again for every row tile, the chunk kernel computes
+    // 256 rows whatever there is.  Measured on GB300 (n = 4 bf16, 2 kv heads, us, decode / chunk) by
+    // passes over the keys (query heads a kv head x new tokens), 64 sequences of 2000 keys:
+    //   heads of 128: 1 (16 x 1) 95 / 118, 2 (8 x 4) 171 / 118;
+    //   heads of 64:  1 (16 x 1) 57 / 96, 2 (8 x 4) 97 / 96, 3 (9 x 3) 135 / 96, 4 (8 x 8) 176 / 96,
+    // and 16 sequences of 6000 keys: heads of 128: 1 73 / 87, 2 124 / 88; heads of 64: 2 65 / 69, 3 96 / 70.
+    // (One sequence of 4000 keys is faster in the decode kernel up to 4 passes: 23.3 / 23.4, 16.4 / 21.)
+    const bool few = decode_tiles(q_heads / kv->d.kv_heads, b->max_new).passes <= (kv->d.head_dim == 64 ? 2u : 1u);
     if (b->tokens)
         rc = on_device_of(h, [&] {
             return few ? launch_attention_decode(*kv, *b, c, window, (cudaStream_t)stream)

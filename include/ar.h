@@ -582,8 +582,9 @@ int ar_rope_append(ar_kv kv, const ar_batch_t* batch, const void* const* q, cons
  * Scores, softmax statistics and sums are fp32; the probabilities meet the
  * values in the cache's type, rounded to it once for chunks and as a sum of two
  * such parts for few rows per kv head; the output is rounded once at the end.
- * Few rows per kv head (max_new x q_heads / kv_heads up to 16, 32 for heads of
- * 64) and more take different kernels; either is right for every batch, and the
+ * Few rows per kv head (max_new tokens x q_heads / kv_heads heads that fit one
+ * tile of 16 rows, or two for heads of 64, in whole tokens) and more take
+ * different kernels; either is right for every batch, and the
  * result does not depend on how the keys are split over the CTAs in between (the
  * split follows the batch alone, and its parts are joined in one order).
  * ar_traffic reports the queries' and outputs' bytes: the keys are known on the
