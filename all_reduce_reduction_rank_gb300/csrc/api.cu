@@ -40,8 +40,6 @@ bool overlap(const void* a, const void* b, size_t bytes)
     return bytes && x < y + bytes && y < x + bytes;
 }
 
-bool aligned16(const void* p) { return ((uintptr_t)p & 15u) == 0; }
-
 // [a, a + an) and [b, b + bn) intersect.
 bool overlap_sized(const void* a, size_t an, const void* b, size_t bn)
 {
@@ -293,18 +291,6 @@ void plan(int op, int n, size_t count, int dt, ar_traffic_t* t)
         break;
     default: break;
     }
-}
-
-// Runs a launch on the handle's device, restoring the caller's device after.
-template <typename F>
-int on_device(const Handle& h, F&& f)
-{
-    int cur = -1;
-    if (cudaGetDevice(&cur) != cudaSuccess) return AR_ERR_CUDA;
-    if (cur != h.device && cudaSetDevice(h.device) != cudaSuccess) return AR_ERR_CUDA;
-    const int rc = f();
-    if (cur != h.device) cudaSetDevice(cur);
-    return rc;
 }
 
 void free_timing(Timing& t)

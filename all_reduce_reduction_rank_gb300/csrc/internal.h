@@ -152,6 +152,21 @@ inline size_t piece_elems(const Handle& h, uint64_t handed_bytes, size_t len)
     return pl < len ? pl : len;
 }
 
+inline bool aligned16(const void* p) { return ((uintptr_t)p & 15u) == 0; }
+
+// Runs f (a launch, an allocation) on the handle's device, restoring the caller's
+// device after.
+template <typename F>
+int on_device(const Handle& h, F&& f)
+{
+    int cur = -1;
+    if (cudaGetDevice(&cur) != cudaSuccess) return AR_ERR_CUDA;
+    if (cur != h.device && cudaSetDevice(h.device) != cudaSuccess) return AR_ERR_CUDA;
+    const int rc = f();
+    if (cur != h.device) cudaSetDevice(cur);
+    return rc;
+}
+
 // Independent pieces on two streams.  A call's pieces do not depend on each
 // other, so when it has many the call runs twice as many, half as long,
 // alternately on the caller's stream and on the handle's side stream (forked

@@ -21,20 +21,6 @@ constexpr uint32_t kKvMagic = 0x41524b56u;  // "ARKV"
 
 constexpr size_t kMaxStride = (size_t)1 << 39;   // elements: tensor copies take strides below 2^40 bytes
 
-bool aligned16(const void* p) { return ((uintptr_t)p & 15u) == 0; }
-
-// Runs f on the handle's device, restoring the caller's device after.
-template <typename F>
-int on_device_of(const Handle& h, F&& f)
-{
-    int cur = -1;
-    if (cudaGetDevice(&cur) != cudaSuccess) return AR_ERR_CUDA;
-    if (cur != h.device && cudaSetDevice(h.device) != cudaSuccess) return AR_ERR_CUDA;
-    const int rc = f();
-    if (cur != h.device) cudaSetDevice(cur);
-    return rc;
-}
-
 int check_desc(const ar_kv_desc_t* d)
 {
     if (!d) return AR_ERR_INVALID;
@@ -249,7 +235,7 @@ int ar_kv_create(ar_handle hd, const ar_kv_desc_t* d, void* const* k, void* cons
         kv.k[r] = k[r];
         kv.v[r] = v[r];
     }
-    const int rc = on_device_of(*h, [&]() -> int {
+    const int rc = on_device(*h, [&]() -> int {
         void* fn = nullptr;
         cudaDriverEntryPointQueryResult found;
         if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault, &found) !=
@@ -330,7 +316,7 @@ int ar_kv_destroy(ar_kv k)
 {
     KvCache* kv = get(k);
     if (!kv) return AR_ERR_INVALID;
-    const int rc = on_device_of(*kv->h, [&] {
+    const int rc = on_device(*kv->h, [&] {
         int r = cudaDeviceSynchronize() == cudaSuccess ? AR_OK : AR_ERR_CUDA;
         if (cudaFree(kv->maps) != cudaSuccess) r = AR_ERR_CUDA;
         if (cudaFree(kv->partial) != cudaSuccess) r = AR_ERR_CUDA;
@@ -365,7 +351,7 @@ int ar_rope_append(ar_kv k, const ar_batch_t* b, const void* const* q, const voi
     const size_t row = (size_t)kv->d.head_dim * ((size_t)(q ? q_heads : 0) + 2u * (size_t)kv->d.kv_heads);
     int rc = AR_OK;
     h.timing.op = AR_OP_ROPE_APPEND;
-    if (b->tokens) rc = on_device_of(h, [&] { return launch_rope_append(*kv, *b, c, (cudaStream_t)stream); });
+    if (b->tokens) rc = on_device(h, [&] { return launch_rope_append(*kv, *b, c, (cudaStream_t)stream); });
     if (rc != AR_OK) return rc;
     const uint64_t moved = 2ull * h.n * b->tokens * row;
     note(h, AR_OP_ROPE_APPEND, b->tokens * row, moved, moved, (cudaStream_t)stream);
@@ -393,7 +379,7 @@ int ar_paged_attention(ar_kv k, const ar_batch_t* b, const void* const* q, void*
     // (One sequence of 4000 keys is faster in the decode kernel up to 4 passes: 23.3 / 23.4, 16.4 / 21.)
     const bool few = decode_tiles(q_heads / kv->d.kv_heads, b->max_new).passes <= (kv->d.head_dim == 64 ? 2u : 1u);
     if (b->tokens)
-        rc = on_device_of(h, [&] {
+        rc = on_device(h, [&] {
             return few ? launch_attention_decode(*kv, *b, c, window, (cudaStream_t)stream)
                        : launch_attention_chunk(*kv, *b, c, window, (cudaStream_t)stream);
         });

@@ -24,37 +24,12 @@
 // (no CTA-wide barrier anywhere), and pass 2 scales r and writes every rank's
 // output.
 // HBM: reads n S + S (+ the weight, H per launch), writes n S + S.
-#include "common.cuh"
+#include "cluster.cuh"
 
 namespace argb {
 namespace {
 
 constexpr int kClusterCtas = 8;   // the smallest cluster: it sizes the longest slice a CTA keeps
-
-__device__ __forceinline__ uint32_t cluster_ctarank()
-{
-    uint32_t r;
-    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-    return r;
-}
-
-__device__ __forceinline__ uint32_t to_cluster(const void* local, uint32_t cta)
-{
-    uint32_t remote;
-    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;"
-                 : "=r"(remote)
-                 : "r"((uint32_t)__cvta_generic_to_shared(local)), "r"(cta));
-    return remote;
-}
-
-// Write v to CTA `cta`'s shared memory, at the offset of `local` in ours, and
-// count its 4 bytes on that CTA's barrier at the offset of `bar` in ours.
-__device__ __forceinline__ void st_async_cluster_f32(float* local, const uint64_t* bar, uint32_t cta, float v)
-{
-    asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.b32 [%0], %1, [%2];" ::"r"(to_cluster(local, cta)),
-                 "r"(__float_as_uint(v)), "r"(to_cluster(bar, cta))
-                 : "memory");
-}
 
 // Compiled for at least 512 threads per SM (at most 128 registers a thread,
 // no spills at any n).
@@ -71,16 +46,13 @@ allreduce_rmsnorm_kernel(const __grid_constant__ CPtrs<NR> in, const void* __res
     __shared__ float parts[NP];                   // warp w of CTA k sends into parts[k * W + w]
     __shared__ __align__(8) uint64_t parts_bar;   // completes when the NP partials have landed
     if (threadIdx.x == 0) {
-        // one arrival (this one, expecting the partials' bytes), then the bytes
-        const uint32_t bar = (uint32_t)__cvta_generic_to_shared(&parts_bar);
-        asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(bar) : "memory");
-        asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(4u * NP) : "memory");
-        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        cluster_bar_init(&parts_bar, 4u * NP);
+        cluster_bar_init_fence();
     }
     // the first half of a cluster barrier: its wait, before the partial sums
     // are sent, makes sure every CTA of the cluster has started and has set up
     // its barrier
-    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+    cluster_arrive();
     pdl_acquire();
     if (early_release) pdl_release();
     const uint32_t c = cluster_ctarank();
@@ -133,26 +105,12 @@ allreduce_rmsnorm_kernel(const __grid_constant__ CPtrs<NR> in, const void* __res
     for (int o = 16; o > 0; o >>= 1) ss = ss + __shfl_down_sync(0xffffffffu, ss, o);
     ss = __shfl_sync(0xffffffffu, ss, 0);
     const uint32_t lane = threadIdx.x & 31, w = threadIdx.x >> 5;
-    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+    cluster_wait();
     if (lane < CL) st_async_cluster_f32(&parts[c * W + w], &parts_bar, lane, ss);
-    {
-        // every thread waits (bounded) until all NP partials have landed here; a
-        // CTA leaves only after that, so nothing is still landing in its shared
-        // memory when it exits
-        const uint32_t bar = (uint32_t)__cvta_generic_to_shared(&parts_bar);
-        uint32_t done = 0;
-        const uint64_t t0 = globaltimer_ns();
-        for (uint32_t it = 0; it < (1u << 22) && !done; ++it) {
-            asm volatile("{\n\t.reg .pred p;\n\t"
-                         "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], 0;\n\t"
-                         "selp.u32 %0, 1, 0, p;\n\t}"
-                         : "=r"(done)
-                         : "r"(bar)
-                         : "memory");
-            if (!done && (it & 255) == 255 && globaltimer_ns() - t0 > 100000000ull) break;   // 0.1 s
-        }
-        if (!done) report_wait_timeout(st);
-    }
+    // every thread waits (bounded) until all NP partials have landed here; a CTA
+    // leaves only after that, so nothing is still landing in its shared memory when
+    // it exits
+    if (!cluster_bar_wait(&parts_bar)) report_wait_timeout(st);
     // the row's sum, in the same order in every warp: lane j adds parts j, j + 32,
     // ..., then the lanes pairwise down to lane 0
     float t2 = 0.0f;
