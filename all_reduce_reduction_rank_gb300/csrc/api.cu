@@ -545,6 +545,10 @@ int ar_set_option(ar_handle hd, int option, int64_t value)
         if (value < 1 || value > 10000000000LL) return AR_ERR_INVALID;
         h->spin_ns = value;
         return AR_OK;
+    case AR_OPT_ATTENTION_PARTS:
+        if (value != 1 && value != 2) return AR_ERR_INVALID;
+        h->attention_parts = (int)value;
+        return AR_OK;
     case AR_OPT_ONE_SHOT_IMPL:
         if (value < 0 || value > 2) return AR_ERR_INVALID;
         h->one_shot_impl = (int)value;

@@ -39,6 +39,13 @@
 // being multiplied) and its products follow each other.  A row tile costs about 3
 // key tiles more (queries, first scores, last product, output).
 //
+// Probabilities as one part of the cache's type or as two (AR_OPT_ATTENTION_PARTS): two
+// take as many products of the second kind again and the softmax warps' time to make
+// them.  8192 tokens on 8192 2.13 / 3.26 ms, packed prompts 207 / 336 us; error against
+// 64 bits 1.3 to 1.4 times that of fp32 probabilities / the same (packed prompts bf16
+// 2.07e-3 / 1.61e-3).  One is the default: the half step it costs is no more than the
+// output's own rounding.
+//
 // Split of the keys over CTAs: as in the decode kernel (split_work); the parts,
 // up to 128 KB each, are joined by a second launch.
 #include "paged.cuh"
@@ -279,7 +286,7 @@ __device__ void watch_tiles(const ChunkArgs& a, const BatchArgs& b, uint8_t* sta
     }
 }
 
-template <int DT, int D>
+template <int DT, int D, int PARTS>
 __device__ void issue(const ChunkArgs& a, const BatchArgs& b, uint8_t* q_tiles, uint8_t* stages, ChunkShared* sh,
                       DevStatus* st)
 {
@@ -345,9 +352,13 @@ __device__ void issue(const ChunkArgs& a, const BatchArgs& b, uint8_t* q_tiles, 
                     if (ok && elect_one()) {
                         const uint64_t va = mma_operand(smem_addr(stages + v_stage * kTileBytes<D>), 1024, kKeys * 128);
 #pragma unroll
-                        for (int k = 4 * part; k < 4 * part + 4; ++k)
+                        for (int k = 4 * part; k < 4 * part + 4; ++k) {
                             mma_ts(tmem + 2 * kKeys + h * D, tmem + h * kKeys + 8 * k, va + k * (2048 >> 4), kValues,
                                    i > 0 || k > 0);
+                            if constexpr (PARTS == 2)
+                                mma_ts(tmem + 2 * kKeys + h * D, tmem + h * kKeys + kKeys / 2 + 8 * k,
+                                       va + k * (2048 >> 4), kValues, true);
+                        }
                         if (part == 1 && i + 1 == n[h]) mma_commit(&sh->o_full[h]);
                     }
                     __syncwarp();
@@ -422,7 +433,7 @@ __device__ __forceinline__ void transpose4(uint32_t (&w)[4][4], int lane)
     }
 }
 
-template <int DT, int D>
+template <int DT, int D, int PARTS>
 __device__ void soften(const ChunkArgs& a, const BatchArgs& b, ChunkShared* sh, DevStatus* st)
 {
     using T = typename Payload<DT>::scalar_t;
@@ -502,7 +513,7 @@ __device__ void soften(const ChunkArgs& a, const BatchArgs& b, ChunkShared* sh, 
             const uint64_t sc = pack2(a.scale_log2, a.scale_log2), off = pack2(-ref, -ref);
 #pragma unroll
             for (int g = 0; g < 4; ++g) {
-                uint32_t pw[16];
+                uint32_t pw[16], rest[16];
 #pragma unroll
                 for (int k = 0; k < 16; ++k) {
                     float y[2];
@@ -511,10 +522,19 @@ __device__ void soften(const ChunkArgs& a, const BatchArgs& b, ChunkShared* sh, 
                     y[0] = ex2(y[0]);
                     y[1] = ex2(y[1]);
                     l2[k & 1] = add2(l2[k & 1], pack2(y[0], y[1]));
-                    // rounded to the cache's type: the product's operand (at most half a step of it each)
+                    // the product's operand has the cache's type: p rounded to it (at most half a step of it
+                    // each), and with two parts what that left out, in the other half of the scores' place
                     pw[k] = Payload<DT>::narrow(y);
+                    if constexpr (PARTS == 2) {
+                        float back[2];
+                        Payload<DT>::widen(pw[k], back);
+                        back[0] = y[0] - back[0];
+                        back[1] = y[1] - back[1];
+                        rest[k] = Payload<DT>::narrow(back);
+                    }
                 }
                 tmem_st16(s_at + 16 * g, pw);
+                if constexpr (PARTS == 2) tmem_st16(s_at + kKeys / 2 + 16 * g, rest);
                 if (g & 1) {
                     tmem_wait_st();
                     tmem_before_sync();
@@ -603,7 +623,7 @@ __device__ void soften(const ChunkArgs& a, const BatchArgs& b, ChunkShared* sh, 
     }
 }
 
-template <int DT, int D>
+template <int DT, int D, int PARTS>
 __global__ void __launch_bounds__(kTh, 1)
 attention_chunk_kernel(const __grid_constant__ ChunkArgs a, const BatchArgs b, DevStatus* st)
 {
@@ -646,11 +666,11 @@ attention_chunk_kernel(const __grid_constant__ ChunkArgs a, const BatchArgs b, D
     tmem_after_sync();
     if (warp < 8) {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
-        soften<DT, D>(a, b, sh, st);
+        soften<DT, D, PARTS>(a, b, sh, st);
     } else {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
         if (warp == 8)
-            issue<DT, D>(a, b, q_tiles, stages, sh, st);
+            issue<DT, D, PARTS>(a, b, q_tiles, stages, sh, st);
         else if (warp == 9)
             produce<D>(a, b, stages, sh, st);
         else if (warp == 10)
@@ -762,28 +782,32 @@ int launch_attention_chunk(KvCache& kv, const ar_batch_t& b, const AttnCall& c, 
     a.box_tokens = kv.box_tokens;
     a.min_units = 4;
     const uint64_t moved = (uint64_t)h.n * b.tokens * c.q_heads * kv.d.head_dim * 2u * 2u;
-    auto run = [&](auto dtc, auto dc) -> int {
-        constexpr int DT = decltype(dtc)::value, D = decltype(dc)::value;
+    auto run = [&](auto dtc, auto dc, auto pc) -> int {
+        constexpr int DT = decltype(dtc)::value, D = decltype(dc)::value, PARTS = decltype(pc)::value;
         static std::atomic<uint32_t> attr_done{0};
         if (!once_per_device(attr_done, [&] {
-                return cudaFuncSetAttribute(attention_chunk_kernel<DT, D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                return cudaFuncSetAttribute(attention_chunk_kernel<DT, D, PARTS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                             kSmem<D>) == cudaSuccess;
             }))
             return AR_ERR_CUDA;
         rec_begin(h, s);
-        const cudaError_t e = launch_kernel(h, attention_chunk_kernel<DT, D>, dim3((unsigned)h.sm_count), dim3(kTh),
+        const cudaError_t e = launch_kernel(h, attention_chunk_kernel<DT, D, PARTS>, dim3((unsigned)h.sm_count), dim3(kTh),
                                             kSmem<D>, s, a, batch_args(kv, b, window), h.status);
         const cudaError_t e2 = launch_kernel(h, attention_join_kernel<DT, D>,
                                              dim3((unsigned)h.sm_count, 2 * D / kJoinColumns), dim3(kHalf), 0, s, a);
         rec_end(h, s, AR_K_ATTENTION_CHUNK, moved, 2);
         return e == cudaSuccess && e2 == cudaSuccess ? launch_status() : AR_ERR_CUDA;
     };
+    auto parts = [&](auto dtc, auto dc) -> int {
+        return h.attention_parts == 2 ? run(dtc, dc, std::integral_constant<int, 2>{})
+                                      : run(dtc, dc, std::integral_constant<int, 1>{});
+    };
     using BF = std::integral_constant<int, AR_BF16>;
     using HF = std::integral_constant<int, AR_F16>;
     using D64 = std::integral_constant<int, 64>;
     using D128 = std::integral_constant<int, 128>;
-    if (kv.d.dtype == AR_BF16) return kv.d.head_dim == 128 ? run(BF{}, D128{}) : run(BF{}, D64{});
-    return kv.d.head_dim == 128 ? run(HF{}, D128{}) : run(HF{}, D64{});
+    if (kv.d.dtype == AR_BF16) return kv.d.head_dim == 128 ? parts(BF{}, D128{}) : parts(BF{}, D64{});
+    return kv.d.head_dim == 128 ? parts(HF{}, D128{}) : parts(HF{}, D64{});
 }
 
 }  // namespace argb

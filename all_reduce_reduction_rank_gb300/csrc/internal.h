@@ -39,6 +39,7 @@ struct Handle {
     int l2_bytes = 0;   // the device's L2 size
     int ctas_per_sm = 0;  // 0: one full wave, from each kernel's occupancy
     int64_t spin_ns = 1000000;
+    int attention_parts = 1;
     int one_shot_impl = 0;
     int pdl = 1;  // programmatic dependent launch between consecutive kernels
     int auto_policy = AR_AUTO_MODEL;

@@ -175,6 +175,10 @@ enum {
                                 kernel boundary separates the phases); 2 one launch, each CTA
                                 gathering the tile it reduced after a CTA barrier; 3 one launch,
                                 tiles handed between CTAs by ready flags; 0 (default): 2 */
+    AR_OPT_ATTENTION_PARTS = 16,/* parts of the cache's type as which the chunk kernel of
+                                ar_paged_attention feeds the probabilities: 1 (default), rounded
+                                once; 2, with what that left out, as its decode kernel always does
+                                (error as with fp32 probabilities, about 1.5 times the time) */
     AR_OPT_PDL = 6           /* 1 (default): launch with programmatic stream
                                 serialization, so a kernel is scheduled while the one
                                 before it in the stream drains (each kernel waits for
@@ -580,8 +584,9 @@ int ar_rope_append(ar_kv kv, const ar_batch_t* batch, const void* const* q, cons
  * the window of a sequence's first new token, may hold anything, NaN included.
  * A non-finite value within them may reach every row of the sequence.
  * Scores, softmax statistics and sums are fp32; the probabilities meet the
- * values in the cache's type, rounded to it once for chunks and as a sum of two
- * such parts for few rows per kv head; the output is rounded once at the end.
+ * values in the cache's type, rounded to it once for chunks (AR_OPT_ATTENTION_PARTS)
+ * and as a sum of two such parts for few rows per kv head; the output is rounded
+ * once at the end.
  * Few rows per kv head (max_new tokens x q_heads / kv_heads heads that fit one
  * tile of 16 rows, or two for heads of 64, in whole tokens) and more take
  * different kernels; either is right for every batch, and the

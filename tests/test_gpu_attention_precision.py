@@ -1,5 +1,6 @@
 """The decode kernel feeds the probabilities to the second product as two parts
-of the cache's type, so its outputs carry no half step of that type for them.
+of the cache's type, the chunk kernel too with AR_OPT_ATTENTION_PARTS = 2, so their
+outputs carry no half step of that type for them.
 
 Few keys with nearly equal scores, whose values differ in sign alone: outputs
 are small beside sum p |v|, and a half step of the probabilities, u sum p |v|, would
@@ -15,7 +16,7 @@ import torch
 import all_reduce_reduction_rank_gb300 as ar
 from layer_util import HALF_STEP, TINY, TORCH, Layer, f64
 from oracle import layer
-from test_gpu_paged_attention import run
+from test_gpu_paged_attention import compare, run
 
 
 def tolerance(dtype, dim, keys, want, size, dots, top, vmax):
@@ -34,20 +35,17 @@ def alternating(v):
 KEYS = [2, 4, 8]
 
 
-@pytest.mark.gpu
-@pytest.mark.parametrize("dtype", ["bf16", "f16"])
-@pytest.mark.parametrize("dim", [64, 128])
-@pytest.mark.parametrize("group", [1, 4, 8, 12, 16])      # row tiles of 8 and of 16
-def test_probabilities_lose_nothing_in_the_decode_kernel(group, dim, dtype):
-    with Layer(2, 1, dim, 16, dtype, [1] * len(KEYS), KEYS, seed=group) as L:
+def check(kernel, group, dim, dtype, max_new, parts):
+    with Layer(2, 1, dim, 16, dtype, [1] * len(KEYS), KEYS, seed=group, max_new=max_new) as L:
         for r in range(2):
             for s, n in enumerate(KEYS):
                 L.vals[r][s] = alternating(L.vals[r][s])
                 for j in range(0, n, 16):
                     L.vview[r][int(L.table[s, j // 16]), :, : min(16, n - j)] = L.vals[r][s][j: j + 16].transpose(0, 1).cuda()
         assert ar.ar_set_option(L.h, ar.AR_OPT_TIMING, 1) == ar.AR_OK
+        assert ar.ar_set_option(L.h, ar.AR_OPT_ATTENTION_PARTS, parts) == ar.AR_OK
         q, out = run(L, group, q=[t / 16 for t in L.rows(group)])
-        assert ar.ar_timing(L.h)[0][0] == "attention_decode"
+        assert ar.ar_timing(L.h)[0][0] == "attention_" + kernel
         for r in range(2):
             for s, n in enumerate(KEYS):
                 x = f64(q[r][s: s + 1, : group * dim]).reshape(1, group, dim)
@@ -56,6 +54,40 @@ def test_probabilities_lose_nothing_in_the_decode_kernel(group, dim, dtype):
                 got = f64(out[r][s: s + 1, : group * dim]).reshape(want.shape)
                 tol = tolerance(dtype, dim, n, want, size, dots, top, np.abs(v).max())
                 assert (np.abs(got - want) <= tol).all(), (r, s, np.max(np.abs(got - want) / tol))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("group", [1, 4, 8, 12, 16])      # row tiles of 8 and of 16
+def test_probabilities_lose_nothing_in_the_decode_kernel(group, dim, dtype):
+    check("decode", group, dim, dtype, 1, 1)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("group", [1, 7])
+def test_probabilities_lose_nothing_as_two_parts_in_the_chunk_kernel(group, dim, dtype):
+    check("chunk", group, dim, dtype, 500, 2)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype,dim,window", [("bf16", 128, 0), ("f16", 64, 100), ("f16", 128, 0), ("bf16", 64, 0)])
+@pytest.mark.parametrize("new,kv", [([130, 1, 40], [500, 260, 40]), ([513], [640]), ([2, 1], [20000, 3333])])
+def test_two_parts_give_the_definition(new, kv, dtype, dim, window):
+    first = [max(0, x - q - window + 1) if window else 0 for q, x in zip(new, kv)]
+    with Layer(2, 1, dim, 32, dtype, new, kv, max_new=500, first_kept=first) as L:
+        assert ar.ar_set_option(L.h, ar.AR_OPT_ATTENTION_PARTS, 2) == ar.AR_OK
+        q, out = run(L, 5, window=window)
+        compare(L, q, out, 5, dim**-0.5, window)
+
+
+@pytest.mark.gpu
+def test_the_number_of_parts_is_checked():
+    with Layer(2, 1, 64, 16, "bf16", [1], [3]) as L:
+        for bad in (0, 3, -1):
+            assert ar.ar_set_option(L.h, ar.AR_OPT_ATTENTION_PARTS, bad) == ar.AR_ERR_INVALID
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f16"])
