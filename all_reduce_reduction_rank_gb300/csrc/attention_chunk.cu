@@ -18,7 +18,8 @@
 //                   issuing a product takes as long as the product, so every wait that
 //                   warp 8 does not need shortens the loop
 // The last four warps hand registers to the softmax warps, whose threads hold a
-// row of 128 scores.
+// row of 128 scores.  ptxas still spills (112 to 120 bytes a thread; with two parts 132 to
+// 196): about 8 loads and 3 stores a warp and key tile, among some 1400 instructions.
 //
 // Tensor memory (512 columns): S/P of both halves, O of both halves.  Products
 // run in the order they are issued, and a half's S of tile j + 1 is issued
@@ -31,9 +32,9 @@
 // at the start of a row and hardly ever later.
 //
 // Measured on GB300 (n = 8 bf16, heads of 128): 8192 tokens behind 8192 with 64
-// query heads 2.08 to 2.25 ms from run to run, 1470 to 1590 TFLOP/s (77 to 83%
+// query heads 2.13 to 2.29 ms from run to run, 1440 to 1550 TFLOP/s (76 to 81%
 // of cuBLAS's burst rate); packed prompts of 4096, 1023, 2501 and 577 tokens with 32
-// query heads 205 us, 975 TFLOP/s.  A key tile of both halves takes about 3000
+// query heads 207 us, 966 TFLOP/s.  A key tile of both halves takes about 3000
 // cycles, of them 2048 of products: softmax of a half (scores out of tensor memory
 // 170, maxima 390, exponentials 950, of which the first half of the keys is already
 // being multiplied) and its products follow each other.  A row tile costs about 3

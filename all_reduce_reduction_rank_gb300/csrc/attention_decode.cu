@@ -17,10 +17,10 @@
 // Measured on GB300 (n = 8 bf16, heads of 128, 8 query heads a kv head): 64
 // sequences of 1 to 8192 keys, 792 MB: 127 us, 6.25 TB/s (93% of the copy rate); 4
 // sequences of 70 to 131 thousand keys (n = 4 fp16, 1.77 GB): 258 us, 6.86 TB/s
-// (103%); one sequence of 1500 keys: 8.5 to 9.1 us, where launch, split, page, copy, two
+// (103%); one sequence of 1500 keys: 8.6 to 9.2 us, where launch, split, page, copy, two
 // tiles and the join follow one another.  Short sequences are bound by the same
 // chain per row tile (64 sequences of 300 keys: 25 us for 12.5 us of bytes); the
-// tensor pipe is 17% busy with 16 rows, the warps wait for one another's results.
+// tensor pipe is 14% busy at long ones, the warps wait for one another's results.
 //
 // Softmax in one pass, base 2: with x = scale log2(e) (q . k), a running
 // reference m, p = 2^(x - m), l = sum p, o = sum p v.  m moves only when a row's

@@ -572,8 +572,8 @@ int ar_rope_append(ar_kv kv, const ar_batch_t* batch, const void* const* q, cons
                    size_t q_out_stride, const float* cos_sin, size_t max_positions, int rot_dim, int interleaved,
                    ar_stream_t stream);
 
-/* Causal attention of the new tokens over the caches, one launch for all
- * ranks: the token at position p attends to the keys at positions j <= p, and
+/* Causal attention of the new tokens over the caches, for all ranks in one
+ * launch (few rows per kv head) or two (chunks): the token at position p attends to the keys at positions j <= p, and
  * j > p - window if window > 0, of its sequence:
  *   out = sum_j softmax_j(scale * q . k_j) v_j
  * with query head h on kv head h / (q_heads / kv_heads).  A token that sees no
