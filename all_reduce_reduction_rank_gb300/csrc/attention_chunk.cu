@@ -145,7 +145,7 @@ __device__ __forceinline__ bool next_segment(const BatchArgs& b, int tile_tokens
 __device__ __forceinline__ void warp_wait(bool& ok, uint64_t* bar, uint32_t parity, ChunkShared* sh, DevStatus* st)
 {
     if (__all_sync(0xffffffffu, mbar_wait_20us(bar, parity))) return;
-    if (ok) ok = wait_or_give_up(bar, parity, &sh->gave_up, st);
+    if (ok) ok = wait_on_or_give_up(bar, parity, &sh->gave_up, st);
     ok = __all_sync(0xffffffffu, ok);
 }
 

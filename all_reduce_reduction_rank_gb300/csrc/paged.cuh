@@ -446,6 +446,7 @@ __device__ __forceinline__ bool mbar_wait_20us(uint64_t* bar, uint32_t parity)
 __device__ __forceinline__ bool wait_a_second(uint64_t* bar, uint32_t parity, volatile int* stop)
 {
     const uint64_t t0 = globaltimer_ns();
+#pragma unroll 1
     for (uint32_t i = 0; i < kMbarMaxPolls; ++i) {
         if (mbar_wait_20us(bar, parity)) return true;
         if ((stop && *stop) || globaltimer_ns() - t0 > 1000000000ull) return false;
@@ -453,15 +454,20 @@ __device__ __forceinline__ bool wait_a_second(uint64_t* bar, uint32_t parity, vo
     return false;
 }
 
-// The same for the warps of a CTA that depend on one another: it also ends
-// once another warp has given up, and giving up sets the status word.
-__device__ __forceinline__ bool wait_or_give_up(uint64_t* bar, uint32_t parity, volatile int* gave_up, DevStatus* st)
+// The same for the warps of a CTA that depend on one another, after a first
+// mbar_wait_20us, the usual end: it also ends once another warp has given up, and
+// giving up sets the status word.
+__device__ __forceinline__ bool wait_on_or_give_up(uint64_t* bar, uint32_t parity, volatile int* gave_up, DevStatus* st)
 {
-    if (mbar_wait_20us(bar, parity)) return true;   // the usual end: the clock is not read
     if (wait_a_second(bar, parity, gave_up)) return true;
     *gave_up = 1;
     report_wait_timeout(st);
     return false;
+}
+
+__device__ __forceinline__ bool wait_or_give_up(uint64_t* bar, uint32_t parity, volatile int* gave_up, DevStatus* st)
+{
+    return mbar_wait_20us(bar, parity) || wait_on_or_give_up(bar, parity, gave_up, st);
 }
 
 // Before a CTA ends, whoever issued asynchronous work of it waits for that work,
@@ -477,6 +483,7 @@ __device__ __forceinline__ void wait_for_own(uint64_t* bar, uint32_t parity, Dev
 __device__ __forceinline__ void wait_for_ring(uint64_t* full, int stages, uint32_t issued, int stage, uint32_t phase,
                                               DevStatus* st)
 {
+#pragma unroll 1
     for (uint32_t k = 0; k < issued && k < (uint32_t)stages; ++k) {
         if (--stage < 0) {
             stage = stages - 1;
