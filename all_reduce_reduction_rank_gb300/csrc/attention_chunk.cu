@@ -32,9 +32,9 @@
 // at the start of a row and hardly ever later.
 //
 // Measured on GB300 (n = 8 bf16, heads of 128): 8192 tokens behind 8192 with 64
-// query heads 2.13 to 2.29 ms from run to run, 1440 to 1550 TFLOP/s (76 to 81%
+// query heads 2.08 to 2.24 ms from run to run, 1470 to 1590 TFLOP/s (77 to 83%
 // of cuBLAS's burst rate); packed prompts of 4096, 1023, 2501 and 577 tokens with 32
-// query heads 207 us, 966 TFLOP/s.  A key tile of both halves takes about 3000
+// query heads 200 to 203 us, 985 TFLOP/s.  A key tile of both halves takes about 3000
 // cycles, of them 2048 of products: softmax of a half (scores out of tensor memory
 // 170, maxima 390, exponentials 950, of which the first half of the keys is already
 // being multiplied) and its products follow each other.  A row tile costs about 3
@@ -42,7 +42,7 @@
 //
 // Probabilities as one part of the cache's type or as two (AR_OPT_ATTENTION_PARTS): two
 // take as many products of the second kind again and the softmax warps' time to make
-// them.  8192 tokens on 8192 2.13 / 3.26 ms, packed prompts 207 / 336 us; error against
+// them.  8192 tokens on 8192 2.08 / 3.36 ms, packed prompts 199 / 327 us; error against
 // 64 bits 1.3 to 1.4 times that of fp32 probabilities / the same (packed prompts bf16
 // 2.07e-3 / 1.61e-3).  One is the default: the half step it costs is no more than the
 // output's own rounding.

@@ -178,7 +178,7 @@ enum {
     AR_OPT_ATTENTION_PARTS = 16,/* parts of the cache's type as which the chunk kernel of
                                 ar_paged_attention feeds the probabilities: 1 (default), rounded
                                 once; 2, with what that left out, as its decode kernel always does
-                                (error as with fp32 probabilities, about 1.5 times the time) */
+                                (error as with fp32 probabilities, about 1.6 times the time) */
     AR_OPT_PDL = 6           /* 1 (default): launch with programmatic stream
                                 serialization, so a kernel is scheduled while the one
                                 before it in the stream drains (each kernel waits for
