@@ -117,18 +117,44 @@ int check_apart(int n, const ar_kv_desc_t& d, void* const* k, void* const* v, co
     return AR_OK;
 }
 
+// Some slot of the cache at a shares an element with one of the cache at b (the same
+// cache: with another of its slots).  Both have the description's strides: the
+// places differ by dp pages, dh heads and dt slots, and for every dh and dt the dp
+// that come near are two.
+bool slots_meet(const ar_kv_desc_t& d, const void* a, const void* b)
+{
+    const int64_t D = d.head_dim, ps = (int64_t)d.page_stride, pages = (int64_t)d.pages;
+    const int64_t apart = ((int64_t)(uintptr_t)a - (int64_t)(uintptr_t)b) / 2;   // elements; both 16-byte aligned
+    const int64_t page = ((int64_t)d.kv_heads - 1) * (int64_t)d.head_stride +
+                         ((int64_t)d.page_size - 1) * (int64_t)d.token_stride + D;
+    const int64_t length = (pages - 1) * ps + page;
+    if (apart >= length || -apart >= length) return false;
+    for (int dh = 1 - d.kv_heads; dh < d.kv_heads; ++dh)
+        for (int dt = 1 - d.page_size; dt < d.page_size; ++dt) {
+            const int64_t r = apart + dh * (int64_t)d.head_stride + dt * (int64_t)d.token_stride;
+            const int64_t below = r / ps - (r % ps < 0 ? 1 : 0);
+            for (int64_t dp = below; dp <= below + 1; ++dp)
+                if (dp > -pages && dp < pages && r - dp * ps < D && dp * ps - r < D &&
+                    !(a == b && dh == 0 && dt == 0 && dp == 0))
+                    return true;
+        }
+    return false;
+}
+
 int check_kv(int n, const ar_kv_desc_t* d, void* const* k, void* const* v)
 {
     if (n < 2 || n > kMaxRanks) return AR_ERR_INVALID;
     if (int rc = check_desc(d)) return rc;
     if (!k || !v) return AR_ERR_INVALID;
-    for (int r = 0; r < n; ++r) {
+    for (int r = 0; r < n; ++r)
         if (!k[r] || !v[r]) return AR_ERR_INVALID;
-        for (int q = 0; q < n; ++q)
-            if (k[r] == v[q] || (q != r && (k[r] == k[q] || v[r] == v[q]))) return AR_ERR_INVALID;
-    }
     for (int r = 0; r < n; ++r)
         if (!aligned16(k[r]) || !aligned16(v[r])) return AR_ERR_ALIGN;
+    if (slots_meet(*d, k[0], k[0])) return AR_ERR_INVALID;
+    const auto cache = [&](int c) { return c < n ? k[c] : v[c - n]; };
+    for (int c = 0; c < 2 * n; ++c)
+        for (int e = 0; e < c; ++e)
+            if (cache(c) == cache(e) || slots_meet(*d, cache(c), cache(e))) return AR_ERR_INVALID;
     return AR_OK;
 }
 

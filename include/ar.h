@@ -504,7 +504,8 @@ int ar_allreduce_block_norm(ar_handle h, const void* const* in, const ar_block_n
  * at  page * page_stride + head * head_stride + slot * token_stride + d
  * elements of k[r] (v[r]), so both [page][head][slot][d] and
  * [page][slot][head][d] orders, and caches that keep K and V in one
- * allocation, are described by the strides. */
+ * allocation, are described by the strides.  No two slots share an element,
+ * of one cache or of two. */
 typedef struct {
     int dtype;           /* AR_BF16 or AR_F16 */
     int kv_heads;        /* per rank, 1..1024 */

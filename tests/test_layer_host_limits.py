@@ -66,3 +66,34 @@ def test_rows_between_the_pages_of_a_cache_are_apart():
             ar.AR_ERR_INVALID if tokens > 0 else ar.AR_OK)
     # rows that follow one another reach the next page
     assert apart(rows, d, vs=vs, tokens=2) == ar.AR_OK and apart(rows, d, vs=vs, tokens=3) == ar.AR_ERR_INVALID
+
+
+def test_caches_that_share_elements_are_refused():
+    page, kb = 2 * 16 * 128, 2                       # elements of a page of K, bytes of one
+    ok = lambda d, ks, vs: ar.ar_check_kv(4, d, ks, vs)
+    near = lambda off: [p + off * kb for p in at(0)]
+    # values behind the keys, right behind and one vector too near; keys in the values' last page
+    assert ok(desc(), at(0), near(100 * page)) == ar.AR_OK
+    for off in (100 * page - 8, 99 * page + 64, 8, -8, 128, -100 * page + 8):
+        assert ok(desc(), at(0), near(off)) == ar.AR_ERR_INVALID, off
+    assert ok(desc(), at(0), near(-100 * page)) == ar.AR_OK
+    # two ranks' keys
+    ks = at(0)
+    ks[3] = ks[1] + 5 * page * kb
+    assert ok(desc(), ks, at(1)) == ar.AR_ERR_INVALID
+    # keys and values side by side in each page, in each slot, in each head
+    side = {"page": (dict(ps=2 * page), page), "slot": (dict(ps=2 * page, ts=512, hs=128), 256),
+            "head": (dict(ps=2 * page, ts=128, hs=2 * 16 * 128), 16 * 128),
+            "head of a slot": (dict(ps=2 * page, ts=512, hs=256), 128)}
+    for name, (strides, off) in side.items():
+        assert ok(desc(**strides), at(0), near(off)) == ar.AR_OK, name
+        for more in (8, -8, 120):
+            assert ok(desc(**strides), at(0), near(off + more)) == ar.AR_ERR_INVALID, (name, more)
+
+
+def test_caches_whose_own_slots_overlap_are_refused():
+    ok = lambda **k: ar.ar_check_kv(4, desc(**k), at(0), at(1))
+    assert ok(heads=1, hs=8) == ar.AR_OK and ok(pages=1, ps=8) == ar.AR_OK     # no second head, no second page
+    assert ok(ts=256, hs=128, ps=16 * 256) == ar.AR_OK
+    for bad in (dict(hs=8), dict(hs=120), dict(ps=2 * 16 * 128 - 8), dict(ps=120), dict(ts=136), dict(ts=256, hs=136)):
+        assert ok(**bad) == ar.AR_ERR_INVALID, bad
