@@ -24,7 +24,7 @@ SOURCES = ["api.cu", "one_shot.cu", "two_shot.cu", "ring.cu", "ll.cu", "ring_noa
            "attention_decode_scored.cu", "attention_chunk.cu", "attention_chunk_masked.cu", "attention_chunk_capped.cu",
            "attention_chunk_biased.cu", "attention_chunk_capped_biased.cu", "layer_api.cu"]
 HEADERS = ["common.cuh", "internal.h", "bulk.cuh", "lines.cuh", "cluster.cuh", "block_norm.cuh", "layer.h",
-           "paged.cuh", "tmem.cuh", "attention_decode.cuh", "attention_chunk.cuh"]
+           "paged.cuh", "kv_step.cuh", "tmem.cuh", "attention_decode.cuh", "attention_chunk.cuh"]
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = [

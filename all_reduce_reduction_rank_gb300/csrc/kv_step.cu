@@ -19,6 +19,7 @@
 #include <algorithm>
 
 #include "cluster.cuh"
+#include "kv_step.cuh"
 #include "paged.cuh"
 
 namespace argb {
@@ -49,16 +50,9 @@ struct StepArgs {
     long long* slots;
     int32_t* positions;
     int seqs, tokens, capacity;
-    int longest;                 // tokens that a table row (and 2^30) can hold
+    int longest;                 // tokens that a table row can hold
     int page_shift, pages;
     bool rows_here;
-};
-
-enum : uint32_t { kBad = 1, kSeveralTokens = 2, kSeveralPages = 4 };
-
-struct Sums {
-    uint32_t tokens, take, give;
-    uint32_t flags;
 };
 
 __device__ __forceinline__ uint32_t add_most(uint32_t a, uint32_t b) { return min(a + b, kMost); }
@@ -68,30 +62,10 @@ __device__ __forceinline__ Sums add(const Sums& a, const Sums& b)
     return Sums{add_most(a.tokens, b.tokens), add_most(a.take, b.take), add_most(a.give, b.give), a.flags | b.flags};
 }
 
-// One sequence of the step.
-struct One {
-    int kept, added, old;        // tokens that stay, new ones, tokens before
-    Sums x;
-};
-
 __device__ __forceinline__ One read_one(const StepArgs& a, int s)
 {
-    One o{0, 0, 0, Sums{0, 0, 0, 0}};
-    if (s >= a.seqs) return o;
-    o.old = a.kv_len[s];
-    o.added = a.new_len[s];
-    const bool over = a.done && a.done[s] != 0;
-    o.kept = over ? 0 : o.old;
-    if (o.old < 0 || o.added < 0 || o.old > a.longest || o.added > a.longest - o.kept) {
-        o.x.flags = kBad;
-        return o;
-    }
-    auto pages = [&](int len) { return (uint32_t)(len + (1 << a.page_shift) - 1) >> a.page_shift; };
-    o.x.tokens = (uint32_t)o.added;
-    o.x.give = over ? pages(o.old) : 0u;
-    o.x.take = pages(o.kept + o.added) - pages(o.kept);
-    o.x.flags = (o.added > 1 ? kSeveralTokens : 0u) | (o.x.take > 1 ? kSeveralPages : 0u);
-    return o;
+    if (s >= a.seqs) return One{0, 0, 0, Sums{0, 0, 0, 0}};
+    return one_of(a.kv_len[s], a.new_len[s], a.done && a.done[s] != 0, a.longest, a.page_shift);
 }
 
 struct StepShared {
@@ -209,10 +183,11 @@ kv_step_kernel(const __grid_constant__ StepArgs a, DevStatus* st)
     const int count = *a.free_count;
     const int chunks = (a.seqs + nt - 1) / nt;
     One o = read_one(a, tid);
-    // a single new token in a page that the sequence has: on its way while the sums are taken
+    // a single new token in a page that the sequence has (-1: it does not, or its lengths are
+    // refused): on its way while the sums are taken
+    const int entry = entry_of_one(o, a.page_shift);
     int page = -1;
-    if (a.rows_here && o.added == 1 && o.x.take == 0)
-        page = a.table[(size_t)tid * a.table_stride + (o.kept >> a.page_shift)];
+    if (a.rows_here && entry >= 0) page = a.table[(size_t)tid * a.table_stride + entry];
     Sums in, total;
     if (chunks <= 1) {
         in = scan(o.x, &sh, total);
@@ -387,8 +362,7 @@ int launch_kv_step(KvCache& kv, const ar_kv_step_t& x, uint64_t moved, int* laun
     a.tokens = (int)x.tokens;
     a.capacity = (int)x.capacity;
     a.page_shift = page_shift(kv);
-    const size_t row = x.table_stride << a.page_shift;
-    a.longest = row < (size_t)1 << 30 ? (int)row : 1 << 30;
+    a.longest = longest_row(x.table_stride, a.page_shift);
     a.pages = (int)kv.d.pages;
     const bool rows = x.tokens > 0 && (x.slots || x.positions);
     a.rows_here = rows && x.seqs <= kTh && x.tokens <= kRowsHere;
