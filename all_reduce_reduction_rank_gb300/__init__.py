@@ -246,7 +246,8 @@ def _pair_axis(axes, rot_dim: int) -> bytes | None:
         return None
     if len(axes) < rot_dim // 2:   # the library reads so many
         raise ValueError(f"pair_axis names {len(axes)} axes, rot_dim {rot_dim} has {rot_dim // 2} pairs")
-    return axes if isinstance(axes, bytes) else bytes(axes)
+    # entry by entry: bytes() of an array would be its memory, several bytes an entry
+    return axes if isinstance(axes, bytes) else bytes(list(axes))
 
 
 def _stream(s) -> int | None:
@@ -408,7 +409,7 @@ def ar_rope_append(kv, batch: Batch, qs, ks, vs, q_outs, q_heads: int, q_stride:
 def ar_rope_append_axes(kv, batch: Batch, qs, ks, vs, q_outs, q_heads: int, q_stride: int, kv_stride: int,
                         q_out_stride: int, cos_sin, max_positions: int, rot_dim: int, interleaved: int,
                         axis_positions, axes: int, axis_stride: int, pair_axis, stream=None) -> int:
-    """pair_axis: the axis of each of the rot_dim / 2 pairs, bytes or a list."""
+    """pair_axis: the axis of each of the rot_dim / 2 pairs, bytes or a sequence (list, array, tensor) of whole numbers."""
     return lib().ar_rope_append_axes(kv, ctypes.byref(batch), _pack(qs), _pack(ks), _pack(vs), _pack(q_outs), q_heads,
                                      q_stride, kv_stride, q_out_stride, _addr(cos_sin), max_positions, rot_dim,
                                      interleaved, _addr(axis_positions), axes, axis_stride,
