@@ -501,6 +501,9 @@ __device__ __forceinline__ float unusual_tile(const ScoreArgs& a, float scale_lo
             tmem_ld32(x, s_at);
             tmem_wait_ld();
             if (MODE & kCap) {
+                // (not by near_factor where all are small: scores that no row sees, which may come from what an earlier
+                // call left in shared memory, would choose the polynomial.  Which of these two is run changes nothing
+                // in a score below `far`)
                 auto cap = [&](auto steep) {
 #pragma unroll
                     for (int e = 0; e < kPiece; e += 2) {
@@ -516,13 +519,7 @@ __device__ __forceinline__ float unusual_tile(const ScoreArgs& a, float scale_lo
                 float most = 0.0f;
 #pragma unroll
                 for (int e = 0; e < kPiece; e += 2) most = max3(most, fabsf(x[e]), fabsf(x[e + 1]));
-                if (!__any_sync(0xffffffffu, most >= a.near)) {
-#pragma unroll
-                    for (int e = 0; e < kPiece; e += 2) {
-                        const uint64_t v = pack2(x[e], x[e + 1]);
-                        unpack2(mul2(v, near_factor(a.near_c[0], a.near_c[1], a.near_c[2], v)), x[e], x[e + 1]);
-                    }
-                } else if (__any_sync(0xffffffffu, most >= a.far)) {
+                if (__any_sync(0xffffffffu, most >= a.far)) {
                     cap(std::true_type{});
                 } else {
                     cap(std::false_type{});
@@ -654,7 +651,8 @@ __device__ void soften(const ChunkArgs& a, const BatchOf<MODE>& b, ChunkShared<M
             }
             if (BIAS && !IN_PLACE) steep_bias = __any_sync(0xffffffffu, fabsf(slope) * 31.0f > kLoose);
         }
-        float m = -INFINITY;
+        // (in rows that no query of the sequence is in, padding's or the next one's, m never moves: they decide nothing)
+        float m = MASKED && row >= x.rows ? INFINITY : -INFINITY;
         uint64_t l2[2] = {0ull, 0ull};
         float l_before = 0.0f;   // the sum before the last move of m
         for (int i = 0; i < tiles; ++i) {
@@ -691,7 +689,7 @@ __device__ void soften(const ChunkArgs& a, const BatchOf<MODE>& b, ChunkShared<M
                     for (int g = 0; g < 4; ++g) mx[g] = largest_of<CAP>(s, 32 * g, 32);
                     most = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
                 }
-                if (CAP) unusual |= __any_sync(0xffffffffu, most >= a.scores.near);
+                if (CAP) unusual |= __any_sync(0xffffffffu, m != INFINITY && most >= a.scores.near);
                 if (unusual) {
                     const float away = (float)(key0 - place);
                     largest = CAP || BIAS
@@ -720,7 +718,8 @@ __device__ void soften(const ChunkArgs& a, const BatchOf<MODE>& b, ChunkShared<M
                 } else if constexpr (CAP) {
                     top = unusual ? largest : value(most);
                     // fp16 has not the room: the bound tells that the reference may stay, or the row's maximum is taken
-                    if (DT == AR_F16 && !unusual && __any_sync(0xffffffffu, top > m + (kSlack + kBelow<DT>))) top = value(row_max(s));
+                    if (DT == AR_F16 && !unusual && __any_sync(0xffffffffu, top > m + (kSlack + kBelow<DT>)))
+                        top = value(row_max(s));
                 } else {
                     top = value(row_max(s));
                 }
