@@ -450,7 +450,8 @@ __device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b)
 // In bf16 a bound serves as the row's maximum where there is one for less than a pass over the scores: of a capped
 // score's magnitude (kBound at most, score_args), and of 32 keys' largest score with the nearest one's bias, kLoose bits
 // too much at most (slopes above 1.1 make a tile unusual).  The reference is then up to 60 bits, with a cap and a bias
-// 80, above the row's scores, of the 126 that bf16 and fp32 have below 1.
+// 80, above the row's scores, of the 126 that bf16 and fp32 have below 1: a product under 2^-126 is lost, 2^-46 a key
+// of the output at most.  With two parts, for callers who want fp32's precision, the maximum is taken as in fp16.
 constexpr float kLoose = 50.0f;
 
 constexpr float kHidden = -1e18f;    // where scores are capped: they do not come near it, and its square is finite
@@ -610,7 +611,7 @@ __device__ void soften(const ChunkArgs& a, const BatchOf<MODE>& b, ChunkShared<M
 {
     using B = BatchOf<MODE>;
     constexpr bool MASKED = MODE != kPlain, CAP = MASKED && (MODE & kCap), BIAS = MASKED && (MODE & kBias);
-    constexpr bool IN_PLACE = BIAS && DT == AR_F16;
+    constexpr bool EXACT = DT == AR_F16 || PARTS == 2, IN_PLACE = BIAS && EXACT;
     using T = typename Payload<DT>::scalar_t;
     const int h = threadIdx.x / kHalf, row = threadIdx.x % kHalf, lane = threadIdx.x & 31;
     const uint32_t lanes = (uint32_t)(row & ~31) << 16;
@@ -718,7 +719,7 @@ __device__ void soften(const ChunkArgs& a, const BatchOf<MODE>& b, ChunkShared<M
                 } else if constexpr (CAP) {
                     top = unusual ? largest : value(most);
                     // fp16 has not the room: the bound tells that the reference may stay, or the row's maximum is taken
-                    if (DT == AR_F16 && !unusual && __any_sync(0xffffffffu, top > m + (kSlack + kBelow<DT>)))
+                    if (EXACT && !unusual && __any_sync(0xffffffffu, top > m + (kSlack + kBelow<DT>)))
                         top = value(row_max(s));
                 } else {
                     top = value(row_max(s));

@@ -182,7 +182,8 @@ enum {
     AR_OPT_ATTENTION_PARTS = 16,/* parts of the cache's type as which the chunk kernels of the
                                 attention calls feed the probabilities: 1 (default), rounded
                                 once; 2, with what that left out, as the decode kernels always do
-                                (error as with fp32 probabilities, about 1.6 times the time) */
+                                (error as with fp32 probabilities, about 1.6 times the time; 1.8
+                                where scores are capped) */
     AR_OPT_PDL = 6           /* 1 (default): launch with programmatic stream
                                 serialization, so a kernel is scheduled while the one
                                 before it in the stream drains (each kernel waits for
@@ -693,7 +694,9 @@ int ar_paged_attention(ar_kv kv, const ar_batch_t* batch, const void* const* q, 
  * tokens see are read whoever sees them, and a non-finite key or value among
  * them may reach every row of the sequence.  The fp32 arithmetic's own error
  * aside, a capped score is off by 2^-20 of itself and 8.5e-5 at most (AR_OPT_ATTENTION_PARTS
- * = 2: 6.7e-7).
+ * = 2: 6.7e-7).  Of chunks in bf16, products of a value and its key's probability, as a part of the
+ * row's largest, may count as 0 where they are below 2^-66, with a cap and slopes 2^-46
+ * (AR_OPT_ATTENTION_PARTS = 2, and decode steps: 2^-126).
  * All else is as in ar_paged_attention, the batch's rows behind the last
  * sequence's (q_start[seqs] on: padding) left as they are included. */
 typedef struct {
