@@ -99,8 +99,8 @@ __device__ __forceinline__ MaskedSeq shfl_seq(const MaskedSeq& q, int src)
 
 // Keys of a token at position p end before this: what the causal mask shows (also
 // of the last of several tokens), and the prefix.
-__device__ __forceinline__ int seen_end(const Seq&, int causal_end) { return causal_end > 0 ? causal_end : 0; }
-__device__ __forceinline__ int seen_end(const MaskedSeq& q, int causal_end)
+__host__ __device__ __forceinline__ int seen_end(const Seq&, int causal_end) { return causal_end > 0 ? causal_end : 0; }
+__host__ __device__ __forceinline__ int seen_end(const MaskedSeq& q, int causal_end)
 {
     return causal_end > 0 ? max(causal_end, q.prefix) : 0;
 }
@@ -161,13 +161,13 @@ __host__ __device__ __forceinline__ Span span_of(const Seq& q, int tm, int t, in
 
 // A row tile's span in the batch; the first keys of its tokens never decrease.
 template <int KT>
-__device__ __forceinline__ Span tile_span(const BatchArgs& b, const Seq& q, int tm, int t)
+__host__ __device__ __forceinline__ Span tile_span(const BatchArgs& b, const Seq& q, int tm, int t)
 {
     return span_of<KT>(q, tm, t, b.window);
 }
 
 template <int KT>
-__device__ __forceinline__ Span tile_span(const MaskedBatchArgs& b, const MaskedSeq& q, int tm, int t)
+__host__ __device__ __forceinline__ Span tile_span(const MaskedBatchArgs& b, const MaskedSeq& q, int tm, int t)
 {
     Span p = span_of<KT>(q, tm, t, b.window);
     p.key_hi = seen_end(q, p.key_hi);
@@ -192,13 +192,13 @@ __host__ __device__ __forceinline__ u64 units_of_sequence(const Seq& q, int tm, 
 }
 
 template <typename S>
-__device__ __forceinline__ u64 units_in(const BatchArgs& b, const Seq& q, int tm)
+__host__ __device__ __forceinline__ u64 units_in(const BatchArgs& b, const Seq& q, int tm)
 {
     return units_of_sequence<S>(q, tm, b.window);
 }
 
 template <typename S>
-__device__ __forceinline__ u64 units_in(const MaskedBatchArgs& b, const MaskedSeq& q, int tm)
+__host__ __device__ __forceinline__ u64 units_in(const MaskedBatchArgs& b, const MaskedSeq& q, int tm)
 {
     u64 sum = 0;
     const int nt = (q.nq + tm - 1) / tm;
