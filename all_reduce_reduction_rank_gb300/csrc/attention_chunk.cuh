@@ -18,8 +18,9 @@
 //                   issuing a product takes as long as the product, so every wait that
 //                   warp 8 does not need shortens the loop
 // The last four warps hand registers to the softmax warps, whose threads hold a
-// row of 128 scores.  ptxas still spills (112 to 120 bytes a thread; with two parts 132 to
-// 196): about 8 loads and 3 stores a warp and key tile, among some 1400 instructions.
+// row of 128 scores.  ptxas still spills (plain scores 112 to 120 bytes a thread, with two parts 132 to
+// 196; masks, caps and biases 92 to 204, with two parts 160 to 400): with plain scores about 8 loads
+// and 3 stores a warp and key tile, among some 1400 instructions.
 //
 // Tensor memory (512 columns): S/P of both halves, O of both halves.  Products
 // run in the order they are issued, and a half's S of tile j + 1 is issued
@@ -29,7 +30,8 @@
 //
 // Softmax in one pass, base 2, as in the decode kernel: the reference m moves only
 // when a row's maximum passes it by far (kSlack, kBelow), so O is rescaled a few times
-// at the start of a row and hardly ever later.
+// at the start of a row and hardly ever later.  (Under a bias the keys come from the far end: a
+// row's maximum rises by 185 slopes a tile, and slopes above 0.043 rescale O in every tile.)
 //
 // Measured on GB300 (n = 8 bf16, heads of 128): 8192 tokens behind 8192 with 64
 // query heads 2.08 to 2.24 ms from run to run, 1470 to 1590 TFLOP/s (77 to 83%
@@ -75,8 +77,10 @@ static_assert(256 * kSoftmaxRegs<kPlain> + 128 * kOtherRegs<kPlain> == 384 * 168
 
 // weight of a row tile's start and end: 2 / 3 / 4 key tiles, packed prompts 208.5 / 204 /
 // 203.6 us, 117 tokens on 7752 keys 32.9 / 30.3 / 35.6 us
-// Masks and scores of the call's own (weight 3 and 5 / 3 and 8 / 4 and 12 key tiles): packed documents 144 / 140 /
-// 142 us, with a cap 197 / 187 / 180, prompts with prefixes and a cap 203 / 202 / 199.
+// Masks and scores of the call's own (weight 3 and 5 / 3 and 8 / 4 and 12 key tiles): packed documents 142 / 138 /
+// 143 us, with a cap 196 / 187 / 180; prompts with prefixes 157 / 159 / 165, with a cap 204 / 203 / 200; a chunk of 512
+// with 15 decodes 43 / 43 / 43, with a cap 48.3 / 48.3 / 46.7, with a bias too 55.3 / 55.5 / 54.4; 1000 tokens on 8000
+// 218 / 220 / 221, with a cap 240 / 240 / 242; 8192 on 8192 within 1% with masks, caps, biases and both.
 template <int MODE>
 using ChunkSplit = std::conditional_t<MODE == kPlain, Split<kKeys, 3, 5>,
                                       std::conditional_t<(MODE & kCap) != 0, Split<kKeys, 4, 12>, Split<kKeys, 3, 8>>>;
@@ -444,8 +448,10 @@ __device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b)
 // Bound by the same chain as the plain kernel, with more for the softmax to do: a cap is two fused products and a
 // square for two scores beside the exponentials, a bias two products a score.  Measured (n = 8 bf16, 64 heads of 128,
 // scores of N(0, 1), 8192 tokens on 8192, where the plain kernel takes 2.09 ms): masks alone 2.2 ms, cap 50 2.35 (1400
-// TFLOP/s; fp16 2.55), bias 2.59, both 3.21; cap 10, where some warps have large scores, 3.18, cap 5, where all have,
-// 6.12.  Packed documents of about 700 tokens 138 us, prompts with prefixes and a cap 198.
+// TFLOP/s; fp16 2.5 to 2.6), bias 2.6, both 3.22; two parts: cap 50 4.2, bias 4.15, both 5.08.  A cap is cheap while
+// scores are small beside it: cap 30 2.38, 20 2.42, 10, where some warps have large scores, 3.16, 5, where all have,
+// 5.8; cap 50 with scores of N(0, 4), N(0, 16), N(0, 64), N(0, 256) 2.37, 3.24, 5.33, 7.15.  Packed documents of about
+// 700 tokens 116 to 137 us by where they begin, prompts with prefixes and a cap 199.
 
 // In bf16 a bound serves as the row's maximum where there is one for less than a pass over the scores: of a capped
 // score's magnitude (kBound at most, score_args), and of 32 keys' largest score with the nearest one's bias, kLoose bits
@@ -502,9 +508,9 @@ __device__ __forceinline__ float unusual_tile(const ScoreArgs& a, float scale_lo
             tmem_ld32(x, s_at);
             tmem_wait_ld();
             if (MODE & kCap) {
-                // (not by near_factor where all are small: scores that no row sees, which may come from what an earlier
-                // call left in shared memory, would choose the polynomial.  Which of these two is run changes nothing
-                // in a score below `far`)
+                // Which of the two is run changes nothing in a score below `far`, so that scores that no row sees, which
+                // may come from what an earlier call left in shared memory, decide nothing.  (near_factor for pieces of
+                // small scores would: its results differ.)
                 auto cap = [&](auto steep) {
 #pragma unroll
                     for (int e = 0; e < kPiece; e += 2) {

@@ -558,6 +558,11 @@ static int attention(ar_kv k, const ar_batch_t* b, const AttnCall& c, bool score
     //   heads of 64:  1 (16 x 1) 57 / 96, 2 (8 x 4) 97 / 96, 3 (9 x 3) 135 / 96, 4 (8 x 8) 176 / 96,
     // and 16 sequences of 6000 keys: heads of 128: 1 73 / 87, 2 124 / 88; heads of 64: 2 65 / 69, 3 96 / 70.
     // (One sequence of 4000 keys is faster in the decode kernel up to 4 passes: 23.3 / 23.4, 16.4 / 21.)
+    // Scored calls go by the same rule.  64 sequences of 2000 keys, with a cap, with a cap and a bias:
+    //   heads of 128: 1 97 / 145, 101 / 175, 2 173 / 145, 181 / 176;
+    //   heads of 64:  1 64 / 123, 68 / 149, 2 113 / 122, 121 / 149, 3 161 / 123, 174 / 150, 4 211 / 122, 228 / 150,
+    // and 16 sequences of 6000 keys: heads of 128: 1 75 / 98, 76 / 118, 2 128 / 98, 130 / 118; heads of 64:
+    // 2 79 / 83, 86 / 102, 3 115 / 83, 124 / 103.  (One of 4000: 21.6 / 28.7 at 2 passes, 25.9 / 28.8 at 4.)
     const bool few = decode_tiles(c.q_heads / kv->d.kv_heads, b->max_new).passes <= (kv->d.head_dim == 64 ? 2u : 1u);
     if (b->tokens)
         rc = on_device(h, [&] {

@@ -644,7 +644,8 @@ int ar_rope_append(ar_kv kv, const ar_batch_t* batch, const void* const* q, cons
  *   one axis); pair_axis: HOST array of R/2 axes, copied
  *   into the launch; R = rot_dim is not 0.
  * Tokens behind the last sequence's (q_start[seqs] <= t: a step padded to a fixed
- * number of rows) are left out and nothing of them is looked at.  A token with a
+ * number of rows) are left out: their rows and positions are memory that may be
+ * read, whatever it holds.  A token with a
  * position outside 0 .. max_positions - 1 on any of the axes is left out and sets
  * AR_ERR_INDEX. */
 int ar_rope_append_axes(ar_kv kv, const ar_batch_t* batch, const void* const* q, const void* const* k,
